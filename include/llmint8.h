@@ -53,7 +53,8 @@ typedef enum llmint8_status {
     LLMINT8_ERR_HIP = 3               /* a HIP call or launch failed; see llmint8_last_hip_error */
 } llmint8_status;
 
-typedef enum llmint8_dtype { LLMINT8_F16 = 0, LLMINT8_BF16 = 1 } llmint8_dtype;
+/* LLMINT8_F32 is a type of router logits only */
+typedef enum llmint8_dtype { LLMINT8_F16 = 0, LLMINT8_BF16 = 1, LLMINT8_F32 = 2 } llmint8_dtype;
 
 #define LLMINT8_K_ALIGN 64
 #define LLMINT8_K_MAX 133120 /* largest multiple of 64 with K * 127^2 < 2^31 */
@@ -339,6 +340,132 @@ llmint8_status llmint8_linear_fp8_profiled(const void* X, int dtype, int64_t M, 
                                            void* workspace, size_t workspace_bytes,
                                            hipStream_t stream, hipEvent_t start,
                                            hipEvent_t stop);
+
+/*
+ * ---- FP8 (E4M3) with a scale per block of 128 ------------------------------
+ * The same E4M3 codes with finer scales, and no outlier columns: a large value
+ * only coarsens its own block.  Activations have one scale per 128 consecutive
+ * features of a token row, weights one per 128 x 128 block (the last block of a
+ * row or column may be smaller).  With a the largest magnitude of a block:
+ *   code  = e4m3(x * (448 / a)): fp32 divide, fp32 multiply, nearest E4M3 value,
+ *           ties to the even code (a == 0: factor 0; a < 1.4e-36, where 448 / a
+ *           overflows: the largest finite factor);
+ *   scale = a, so that a code stands for value(code) * a / 448.  Weights that
+ *           come with a multiplier s per block take scale = 448 * s.
+ * Sizes, dtypes, pointers, streams and errors follow the conventions at the top
+ * of this file; inputs are finite.  Nothing here has a gradient: the weights
+ * are codes.
+ */
+#define LLMINT8_BLOCK 128
+#define LLMINT8_BLOCK_N_MAX (1 << 30) /* largest N of the block-scaled entry points */
+
+/* Weight codes of `batch` matrices, one after another:
+ *   W [batch,N,K] 16-bit, CB [batch,N,K] uint8 out,
+ *   SCB [batch, ceil(N/128), ceil(K/128)] fp32 out.
+ * batch * ceil(N/128) * ceil(K/128) must be below 2^24 (else UNSUPPORTED). */
+llmint8_status llmint8_quantize_weight_fp8_block(const void* W, int dtype, int64_t batch,
+                                                 int64_t N, int64_t K, uint8_t* CB, float* SCB,
+                                                 hipStream_t stream);
+
+/* Activation codes: X [M,K] 16-bit, CA [M,K] uint8 out, SCA [ceil(K/128), M] fp32
+ * out (block-major: the scales of one block of all rows are adjacent). */
+llmint8_status llmint8_quantize_act_fp8_block(const void* X, int dtype, int64_t M, int64_t K,
+                                              uint8_t* CA, float* SCA, hipStream_t stream);
+
+/* Bytes of device workspace llmint8_matmul_fp8_block needs (may be 0; 0 for
+ * invalid sizes). */
+size_t llmint8_matmul_fp8_block_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Y[m,n] = sum_b SCA[b,m] * SCB[n/128,b] / 448^2
+ *              * (sum over k in block b of value(CA[m,k]) * value(CB[n,k]))  + bias[n],
+ * summed in fp32 and rounded once to Y's 16-bit type.
+ *   CA [M,K], SCA [ceil(K/128), M], CB [N,K], SCB [ceil(N/128), ceil(K/128)];
+ *   bias [N] 16-bit or NULL; Y [M,N] 16-bit out.
+ *   workspace: llmint8_matmul_fp8_block_workspace_size bytes; no initialization.
+ */
+llmint8_status llmint8_matmul_fp8_block(int dtype, int64_t M, int64_t N, int64_t K,
+                                        const uint8_t* CA, const float* SCA, const uint8_t* CB,
+                                        const float* SCB, const void* bias, void* Y,
+                                        void* workspace, size_t workspace_bytes,
+                                        hipStream_t stream);
+
+/* Bytes of device workspace llmint8_linear_fp8_block needs (0 for invalid sizes). */
+size_t llmint8_linear_fp8_block_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* The layer's forward in one call, X [M,K] 16-bit in: the results of
+ * llmint8_quantize_act_fp8_block followed by llmint8_matmul_fp8_block, the
+ * activation codes staying in the workspace
+ * (llmint8_linear_fp8_block_workspace_size bytes). */
+llmint8_status llmint8_linear_fp8_block(const void* X, int dtype, int64_t M, int64_t N, int64_t K,
+                                        const uint8_t* CB, const float* SCB, const void* bias,
+                                        void* Y, void* workspace, size_t workspace_bytes,
+                                        hipStream_t stream);
+
+/*
+ * ---- Mixtures of experts -----------------------------------------------------
+ */
+#define LLMINT8_EXPERTS_MAX 1024
+#define LLMINT8_TOP_K_MAX 32
+#define LLMINT8_GROUPS_MAX 64
+
+typedef enum llmint8_scoring { LLMINT8_SOFTMAX = 0, LLMINT8_SIGMOID = 1 } llmint8_scoring;
+
+/*
+ * Chooses top_k of E experts for each of T tokens.
+ *   logits  [T,E], logits_dtype LLMINT8_F16, LLMINT8_BF16 or LLMINT8_F32; any values.
+ *   score   softmax over the row, or 1 / (1 + exp(-l)) (scoring).
+ *   bias    [E] fp32 or NULL: added to the scores for the choice only.
+ *   n_group, topk_group  the experts form n_group groups of E / n_group
+ *           neighbours, ranked by their best expert or, with a bias, by the sum
+ *           of their two best; only the best topk_group groups are chosen from
+ *           (1, 1: no groups).
+ *   ids     [T,top_k] int32 out: the best experts in order, the lowest index
+ *           first among equals.  Without a bias experts are compared by logit
+ *           (the scores have the same order).
+ *   weights [T,top_k] fp32 out: their scores (without the bias), divided by
+ *           their sum if renormalize != 0, times scale.
+ * An expert whose logit is -inf or NaN, or whose biased score is -inf or NaN, is never
+ * chosen; a slot with no expert left holds id -1 and weight 0 (a row of -inf:
+ * every slot).
+ * Errors: LLMINT8_ERR_INVALID_ARGUMENT for NULL or misaligned pointers, bad
+ * dtype or scoring, E not a multiple of n_group, topk_group outside [1, n_group],
+ * top_k outside [1, topk_group * E / n_group]; LLMINT8_ERR_UNSUPPORTED for
+ * E > LLMINT8_EXPERTS_MAX, top_k > LLMINT8_TOP_K_MAX, n_group > LLMINT8_GROUPS_MAX.
+ * T == 0 is a no-op.
+ */
+llmint8_status llmint8_route_experts(const void* logits, int logits_dtype, int64_t T, int64_t E,
+                                     const float* bias, int scoring, int n_group, int topk_group,
+                                     int top_k, int renormalize, float scale, int32_t* ids,
+                                     float* weights, hipStream_t stream);
+
+/* Bytes of device workspace llmint8_experts_fp8_block needs (0 for invalid sizes). */
+size_t llmint8_experts_fp8_block_workspace_size(int64_t T, int64_t E, int top_k, int64_t K,
+                                                int64_t I);
+
+/*
+ * The experts' feed-forward blocks: for each token t and slot j with expert
+ * e = ids[t,j],
+ *   g = X[t] . W13[e,0]^T,  u = X[t] . W13[e,1]^T,  h = g / (1 + exp(-g)) * u   [I]
+ *   Y[t] = sum_j weights[t,j] * (h . W2[e]^T)                                    [K]
+ * X and h are quantized in blocks of 128 as llmint8_quantize_act_fp8_block does
+ * (h from its fp32 value); all sums are fp32, Y is rounded once.
+ *   X [T,K] 16-bit; ids [T,top_k] int32; weights [T,top_k] fp32;
+ *   CB13 [E,2,I,K] (gate, up), SCB13 [E,2,ceil(I/128),ceil(K/128)];
+ *   CB2 [E,K,I], SCB2 [E,ceil(K/128),ceil(I/128)]; Y [T,K] 16-bit out.
+ *   workspace: llmint8_experts_fp8_block_workspace_size bytes; no initialization.
+ * A slot whose id is outside [0, E) adds nothing (padding, an expert that
+ * another device holds); a token with no expert gets zeros.  An expert may
+ * appear more than once in a row of ids.
+ * K and I are multiples of 64; 2 * I * K must be below 2^32, E at most
+ * LLMINT8_EXPERTS_MAX, top_k at most LLMINT8_TOP_K_MAX (else UNSUPPORTED).
+ */
+llmint8_status llmint8_experts_fp8_block(const void* X, int dtype, int64_t T, int64_t K, int64_t I,
+                                         int64_t E, int top_k, const int32_t* ids,
+                                         const float* weights, const uint8_t* CB13,
+                                         const float* SCB13, const uint8_t* CB2,
+                                         const float* SCB2, void* Y, void* workspace,
+                                         size_t workspace_bytes, hipStream_t stream);
 
 /* Diagnostic for the roofline report, not a step of the method: the device's
  * sustained matrix-core rate, the measured ceiling reported beside the

@@ -12,6 +12,9 @@ in the library's HIP kernels):
   calls on torch tensors; torch supplies device memory and the current stream.
 * ``*_fp8``: the FP8 (E4M3) variant of the same decomposition (codes as uint8
   tensors; ``t.view(torch.float8_e4m3fn)`` gives their values).
+* ``*_fp8_block``: E4M3 codes with a scale per 128 features (activations) or per
+  128 x 128 block (weights); ``route_experts`` and ``experts_fp8_block``: the
+  routing and the expert products of a mixture-of-experts block.
 
 The library must be built (``python -m int8_quantized_matmul_row_amd.build``);
 there is no fallback path.
@@ -27,6 +30,10 @@ LIBRARY_PATH = os.path.join(_HERE, "libllmint8.so")
 
 F16 = 0
 BF16 = 1
+F32 = 2       # router logits only
+SOFTMAX = 0
+SIGMOID = 1
+BLOCK = 128   # features (and weight rows) that share a scale in the *_fp8_block calls
 K_ALIGN = 64
 K_MAX = 133120
 SCRATCH_BYTES = 64 << 20  # LLMINT8_SCRATCH_BYTES: the static scratch of llmint8_linear_noalloc
@@ -53,6 +60,15 @@ EXPORTS = (
     "llmint8_linear_fp8_workspace_size",
     "llmint8_linear_fp8",
     "llmint8_linear_fp8_profiled",
+    "llmint8_quantize_weight_fp8_block",
+    "llmint8_quantize_act_fp8_block",
+    "llmint8_matmul_fp8_block_workspace_size",
+    "llmint8_matmul_fp8_block",
+    "llmint8_linear_fp8_block_workspace_size",
+    "llmint8_linear_fp8_block",
+    "llmint8_route_experts",
+    "llmint8_experts_fp8_block_workspace_size",
+    "llmint8_experts_fp8_block",
     "llmint8_peak_mfma",
     "llmint8_status_string",
     "llmint8_last_hip_error",
@@ -111,6 +127,26 @@ def lib() -> ctypes.CDLL:
     L.llmint8_linear_fp8_workspace_size.restype = ctypes.c_size_t
     L.llmint8_linear_fp8.argtypes = lin
     L.llmint8_linear_fp8_profiled.argtypes = lin + [_P, _P]
+    L.llmint8_quantize_weight_fp8_block.argtypes = [_P, _INT, _I64, _I64, _I64, _P, _P, _P]
+    L.llmint8_quantize_act_fp8_block.argtypes = [_P, _INT, _I64, _I64, _P, _P, _P]
+    L.llmint8_matmul_fp8_block_workspace_size.argtypes = [_I64, _I64, _I64]
+    L.llmint8_matmul_fp8_block_workspace_size.restype = ctypes.c_size_t
+    L.llmint8_matmul_fp8_block.argtypes = [_INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P,
+                                           ctypes.c_size_t, _P]
+    L.llmint8_linear_fp8_block_workspace_size.argtypes = [_I64, _I64, _I64]
+    L.llmint8_linear_fp8_block_workspace_size.restype = ctypes.c_size_t
+    L.llmint8_linear_fp8_block.argtypes = [_P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P,
+                                           ctypes.c_size_t, _P]
+    L.llmint8_route_experts.argtypes = [_P, _INT, _I64, _I64, _P, _INT, _INT, _INT, _INT, _INT,
+                                        ctypes.c_float, _P, _P, _P]
+    L.llmint8_experts_fp8_block_workspace_size.argtypes = [_I64, _I64, _INT, _I64, _I64]
+    L.llmint8_experts_fp8_block_workspace_size.restype = ctypes.c_size_t
+    L.llmint8_experts_fp8_block.argtypes = [_P, _INT, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P,
+                                            _P, _P, _P, _P, ctypes.c_size_t, _P]
+    for f in ("llmint8_quantize_weight_fp8_block", "llmint8_quantize_act_fp8_block",
+              "llmint8_matmul_fp8_block", "llmint8_linear_fp8_block", "llmint8_route_experts",
+              "llmint8_experts_fp8_block"):
+        getattr(L, f).restype = _INT
     for f in ("llmint8_quantize_weight", "llmint8_quantize_tensor", "llmint8_quantize_act",
               "llmint8_matmul", "llmint8_matmul_profiled", "llmint8_linear",
               "llmint8_linear_profiled", "llmint8_linear_noalloc", "llmint8_quantize_weight_fp8",
@@ -257,6 +293,56 @@ def llmint8_linear_fp8_profiled(X, dtype, M, N, K, threshold, CB, SCB, bias, Y, 
                                              SCB, bias, Y, CA, SCA, outlier_idx, n_outliers,
                                              X_outlier, C_f32, workspace, workspace_bytes,
                                              stream, start, stop))
+
+
+def llmint8_quantize_weight_fp8_block(W, dtype, batch, N, K, CB, SCB, stream=0):
+    _check("llmint8_quantize_weight_fp8_block",
+           lib().llmint8_quantize_weight_fp8_block(W, dtype, batch, N, K, CB, SCB, stream))
+
+
+def llmint8_quantize_act_fp8_block(X, dtype, M, K, CA, SCA, stream=0):
+    _check("llmint8_quantize_act_fp8_block",
+           lib().llmint8_quantize_act_fp8_block(X, dtype, M, K, CA, SCA, stream))
+
+
+def llmint8_matmul_fp8_block_workspace_size(M, N, K) -> int:
+    return int(lib().llmint8_matmul_fp8_block_workspace_size(M, N, K))
+
+
+def llmint8_matmul_fp8_block(dtype, M, N, K, CA, SCA, CB, SCB, bias, Y, workspace, workspace_bytes,
+                             stream=0):
+    _check("llmint8_matmul_fp8_block",
+           lib().llmint8_matmul_fp8_block(dtype, M, N, K, CA, SCA, CB, SCB, bias, Y, workspace,
+                                          workspace_bytes, stream))
+
+
+def llmint8_linear_fp8_block_workspace_size(M, N, K) -> int:
+    return int(lib().llmint8_linear_fp8_block_workspace_size(M, N, K))
+
+
+def llmint8_linear_fp8_block(X, dtype, M, N, K, CB, SCB, bias, Y, workspace, workspace_bytes,
+                             stream=0):
+    _check("llmint8_linear_fp8_block",
+           lib().llmint8_linear_fp8_block(X, dtype, M, N, K, CB, SCB, bias, Y, workspace,
+                                          workspace_bytes, stream))
+
+
+def llmint8_route_experts(logits, logits_dtype, T, E, bias, scoring, n_group, topk_group, top_k,
+                          renormalize, scale, ids, weights, stream=0):
+    _check("llmint8_route_experts",
+           lib().llmint8_route_experts(logits, logits_dtype, T, E, bias, scoring, n_group,
+                                       topk_group, top_k, renormalize, scale, ids, weights, stream))
+
+
+def llmint8_experts_fp8_block_workspace_size(T, E, top_k, K, I) -> int:
+    return int(lib().llmint8_experts_fp8_block_workspace_size(T, E, top_k, K, I))
+
+
+def llmint8_experts_fp8_block(X, dtype, T, K, I, E, top_k, ids, weights, CB13, SCB13, CB2, SCB2, Y,
+                              workspace, workspace_bytes, stream=0):
+    _check("llmint8_experts_fp8_block",
+           lib().llmint8_experts_fp8_block(X, dtype, T, K, I, E, top_k, ids, weights, CB13, SCB13,
+                                           CB2, SCB2, Y, workspace, workspace_bytes, stream))
 
 
 def llmint8_peak_mfma(fp8, operands, operand_bytes, sink, sink_bytes, blocks, iters, stream=0):
@@ -566,3 +652,182 @@ def linear_fp8(X, CB, SCB, bias=None, threshold: float = 6.0, stream=None, out=N
     else:
         llmint8_linear_fp8_profiled(*args, events[0], events[1])
     return Y, q
+
+
+# ---- FP8 (E4M3) with a scale per block of 128 ------------------------------------
+
+class BlockAct(NamedTuple):
+    CA: object         # uint8 E4M3 codes [M,K]
+    SCA: object        # fp32 [ceil(K/128), M], block-major
+    dtype: int
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _want(t, name, dtype, shape, device):
+    """t is a contiguous tensor of this type and shape on `device`."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
+    _need(t, name, device)
+
+
+def _rows(t, name):
+    _need(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected two dimensions")
+    return t.shape
+
+
+def _out(out, shape, dtype, device, stream):
+    """The caller's output tensor, checked, or a new one."""
+    if out is None:
+        return _empty(shape, dtype, device, stream)
+    _want(out, "out", dtype, shape, device)
+    return out
+
+
+def _block_workspace(workspace, nbytes, device, stream):
+    """(buffer, bytes) of a call that needs nbytes of workspace."""
+    if workspace is not None:
+        return workspace
+    return (None if nbytes == 0 else _empty((nbytes,), _torch().uint8, device, stream)), nbytes
+
+
+def _check_bias(bias, N, dtype16, device):
+    if bias is not None:
+        _want(bias, "bias", dtype16, (N,), device)
+
+
+def quantize_weight_fp8_block(W, stream=None, out=None):
+    """W [..., N, K] fp16/bf16 -> (CB uint8 E4M3 codes [..., N, K],
+    SCB fp32 [..., ceil(N/128), ceil(K/128)]); every matrix of the leading
+    dimensions has its own blocks."""
+    torch = _torch()
+    _need(W, "W")
+    if W.dim() < 2:
+        raise ValueError(f"W is {tuple(W.shape)}, expected at least two dimensions")
+    lead, (N, K) = tuple(W.shape[:-2]), W.shape[-2:]
+    shape, scales = lead + (N, K), lead + (_blocks(N), _blocks(K))
+    CB, SCB = out if out is not None else (None, None)
+    CB = _out(CB, shape, torch.uint8, W.device, stream)
+    SCB = _out(SCB, scales, torch.float32, W.device, stream)
+    batch = 1
+    for d in lead:
+        batch *= d
+    llmint8_quantize_weight_fp8_block(_ptr(W), dtype_code(W), batch, N, K, _ptr(CB), _ptr(SCB),
+                                      _stream(stream))
+    return CB, SCB
+
+
+def quantize_act_fp8_block(X, stream=None, out: Optional[BlockAct] = None):
+    """X [M,K] fp16/bf16 -> BlockAct: codes and block-major scales."""
+    torch = _torch()
+    M, K = _rows(X, "X")
+    code = dtype_code(X)
+    CA = _out(None if out is None else out.CA, (M, K), torch.uint8, X.device, stream)
+    SCA = _out(None if out is None else out.SCA, (_blocks(K), M), torch.float32, X.device, stream)
+    llmint8_quantize_act_fp8_block(_ptr(X), code, M, K, _ptr(CA), _ptr(SCA), _stream(stream))
+    return BlockAct(CA, SCA, code)
+
+
+def matmul_fp8_block(q: BlockAct, CB, SCB, bias=None, out=None, stream=None, workspace=None):
+    """Y [M,N] from quantize_act_fp8_block and quantize_weight_fp8_block outputs, in
+    the 16-bit type q was made from.  workspace: (buffer, bytes) of at least
+    llmint8_matmul_fp8_block_workspace_size bytes; None allocates it."""
+    torch = _torch()
+    M, K = _rows(q.CA, "CA")
+    N = CB.shape[0]
+    dt_t = torch.float16 if q.dtype == F16 else torch.bfloat16
+    dev = q.CA.device
+    _want(q.CA, "CA", torch.uint8, (M, K), dev)
+    _want(q.SCA, "SCA", torch.float32, (_blocks(K), M), dev)
+    _want(CB, "CB", torch.uint8, (N, K), dev)
+    _want(SCB, "SCB", torch.float32, (_blocks(N), _blocks(K)), dev)
+    _check_bias(bias, N, dt_t, dev)
+    Y = _out(out, (M, N), dt_t, dev, stream)
+    ws, nbytes = _block_workspace(workspace, llmint8_matmul_fp8_block_workspace_size(M, N, K), dev,
+                                  stream)
+    llmint8_matmul_fp8_block(q.dtype, M, N, K, _ptr(q.CA), _ptr(q.SCA), _ptr(CB), _ptr(SCB),
+                             _ptr(bias), _ptr(Y), _ptr(ws), nbytes, _stream(stream))
+    return Y
+
+
+def linear_fp8_block(X, CB, SCB, bias=None, out=None, stream=None, workspace=None):
+    """Y [M,N] = X . W^T (+ bias) through block-scaled E4M3 codes in one call, W given
+    as (CB, SCB) from quantize_weight_fp8_block.  workspace: (buffer, bytes) of at
+    least llmint8_linear_fp8_block_workspace_size bytes; None allocates it."""
+    torch = _torch()
+    M, K = _rows(X, "X")
+    N = CB.shape[0]
+    dev = X.device
+    _want(CB, "CB", torch.uint8, (N, K), dev)
+    _want(SCB, "SCB", torch.float32, (_blocks(N), _blocks(K)), dev)
+    _check_bias(bias, N, X.dtype, dev)
+    code = dtype_code(X)
+    Y = _out(out, (M, N), X.dtype, dev, stream)
+    ws, nbytes = _block_workspace(workspace, llmint8_linear_fp8_block_workspace_size(M, N, K), dev,
+                                  stream)
+    llmint8_linear_fp8_block(_ptr(X), code, M, N, K, _ptr(CB), _ptr(SCB), _ptr(bias), _ptr(Y),
+                             _ptr(ws), nbytes, _stream(stream))
+    return Y
+
+
+# ---- mixtures of experts ----------------------------------------------------------
+
+def route_experts(logits, top_k: int, bias=None, scoring: str = "softmax", n_group: int = 1,
+                  topk_group: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None,
+                  out=None):
+    """logits [T,E] fp16/bf16/fp32 -> (ids int32 [T,top_k], weights fp32 [T,top_k]):
+    the experts of each token, best first, and their weights.  scoring: "softmax" or
+    "sigmoid"; bias fp32 [E] or None sees the choice only; n_group / topk_group: keep
+    the best groups of neighbouring experts.  A logit of -inf (or NaN) takes the
+    expert out; a slot no expert is left for holds id -1 and weight 0."""
+    torch = _torch()
+    T, E = _rows(logits, "logits")
+    if scoring not in ("softmax", "sigmoid"):
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+    code = F32 if logits.dtype == torch.float32 else dtype_code(logits)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,), logits.device)
+    ids, weights = out if out is not None else (None, None)
+    ids = _out(ids, (T, top_k), torch.int32, logits.device, stream)
+    weights = _out(weights, (T, top_k), torch.float32, logits.device, stream)
+    llmint8_route_experts(_ptr(logits), code, T, E, _ptr(bias),
+                          SOFTMAX if scoring == "softmax" else SIGMOID, n_group, topk_group, top_k,
+                          1 if renormalize else 0, scale, _ptr(ids), _ptr(weights),
+                          _stream(stream))
+    return ids, weights
+
+
+def experts_fp8_block(X, ids, weights, CB13, SCB13, CB2, SCB2, out=None, stream=None,
+                      workspace=None):
+    """Y [T,K] = sum over a token's slots of weights * FFN_expert(X), the feed-forward
+    blocks being down(silu(gate(x)) * up(x)) on block-scaled E4M3 weights:
+    CB13 [E,2,I,K] (gate, up) with SCB13, CB2 [E,K,I] with SCB2, from
+    quantize_weight_fp8_block.  ids int32 [T,top_k] and weights fp32 as route_experts
+    gives them; an id outside [0, E) adds nothing.  workspace: (buffer, bytes) of at
+    least llmint8_experts_fp8_block_workspace_size bytes; None allocates it."""
+    torch = _torch()
+    T, K = _rows(X, "X")
+    dev = X.device
+    if CB13.dim() != 4 or CB13.shape[1] != 2:
+        raise ValueError(f"CB13 is {tuple(CB13.shape)}, expected [E, 2, I, K]")
+    E, I = CB13.shape[0], CB13.shape[2]
+    nk, ni = _blocks(K), _blocks(I)
+    _want(CB13, "CB13", torch.uint8, (E, 2, I, K), dev)
+    _want(SCB13, "SCB13", torch.float32, (E, 2, ni, nk), dev)
+    _want(CB2, "CB2", torch.uint8, (E, K, I), dev)
+    _want(SCB2, "SCB2", torch.float32, (E, nk, ni), dev)
+    top_k = _rows(ids, "ids")[1]
+    _want(ids, "ids", torch.int32, (T, top_k), dev)
+    _want(weights, "weights", torch.float32, (T, top_k), dev)
+    code = dtype_code(X)
+    Y = _out(out, (T, K), X.dtype, dev, stream)
+    ws, nbytes = _block_workspace(
+        workspace, llmint8_experts_fp8_block_workspace_size(T, E, top_k, K, I), dev, stream)
+    llmint8_experts_fp8_block(_ptr(X), code, T, K, I, E, top_k, _ptr(ids), _ptr(weights),
+                              _ptr(CB13), _ptr(SCB13), _ptr(CB2), _ptr(SCB2), _ptr(Y), _ptr(ws),
+                              nbytes, _stream(stream))
+    return Y

@@ -288,6 +288,55 @@ llmint8_status quantize_act_impl(const void* X, int dtype, bool fp8, int64_t M, 
     return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
 }
 
+// ---- block-scaled FP8 and experts -------------------------------------------
+
+llmint8_status check_block_sizes(int64_t M, int64_t N, int64_t K) {
+    llmint8_status s = check_sizes(M, N, K);
+    if (s != LLMINT8_OK) return s;
+    return N > LLMINT8_BLOCK_N_MAX ? LLMINT8_ERR_UNSUPPORTED : LLMINT8_OK;
+}
+
+int64_t blocks_of(int64_t n) { return (n + LLMINT8_BLOCK - 1) / LLMINT8_BLOCK; }
+
+bool short_workspace(const void* workspace, size_t bytes, size_t need) {
+    return (workspace && !aligned16(workspace)) || (need > 0 && (workspace == nullptr || bytes < need));
+}
+
+// What the linear layer keeps ahead of the product's workspace: the codes,
+// then their scales.
+struct BlockActLayout {
+    size_t sca, end;
+};
+BlockActLayout block_act_layout(int64_t M, int64_t K) {
+    const size_t sca = align256((size_t)M * K);
+    return {sca, sca + align256((size_t)M * blocks_of(K) * 4)};
+}
+
+llmint8::BlockGemmArgs block_gemm_args(int dtype, int64_t M, int64_t N, int64_t K, const uint8_t* CB,
+                                       const float* SCB, const void* bias, void* Y) {
+    llmint8::BlockGemmArgs a;
+    a.bf16 = dtype == LLMINT8_BF16;
+    a.ld_sa = M;
+    a.CB = CB;
+    a.SCB = SCB;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.bias = static_cast<const uint16_t*>(bias);
+    a.Y = static_cast<uint16_t*>(Y);
+    return a;
+}
+
+llmint8_status check_experts(int64_t T, int64_t E, int top_k, int64_t K, int64_t I) {
+    llmint8_status s = check_sizes(T, E, K);
+    if (s != LLMINT8_OK) return s;
+    if ((s = check_sizes(0, 0, I)) != LLMINT8_OK) return s;
+    if (E < 1 || top_k < 1) return LLMINT8_ERR_INVALID_ARGUMENT;
+    if (E > LLMINT8_EXPERTS_MAX || top_k > LLMINT8_TOP_K_MAX || 2 * I * K >= (int64_t)1 << 32)
+        return LLMINT8_ERR_UNSUPPORTED;
+    return LLMINT8_OK;
+}
+
 }  // namespace
 
 namespace llmint8 {
@@ -467,6 +516,157 @@ llmint8_status llmint8_linear_fp8_profiled(const void* X, int dtype, int64_t M, 
     return linear_impl(X, dtype, true, M, N, K, threshold, reinterpret_cast<const int8_t*>(CB), SCB,
                        bias, Y, reinterpret_cast<int8_t*>(CA), SCA, outlier_idx, n_outliers,
                        X_outlier, nullptr, C_f32, workspace, workspace_bytes, stream, start, stop);
+}
+
+llmint8_status llmint8_quantize_weight_fp8_block(const void* W, int dtype, int64_t batch, int64_t N, int64_t K,
+                                                 uint8_t* CB, float* SCB, hipStream_t stream) {
+    llmint8_status s = check_dtype(dtype);
+    if (s != LLMINT8_OK) return s;
+    if ((s = check_block_sizes(batch, N, K)) != LLMINT8_OK) return s;
+    if (batch == 0 || N == 0) return LLMINT8_OK;
+    if (batch > ((int64_t)1 << 24) / (blocks_of(N) * blocks_of(K))) return LLMINT8_ERR_UNSUPPORTED;
+    if (bad_ptr(W) || bad_ptr(CB) || bad_ptr(SCB)) return LLMINT8_ERR_INVALID_ARGUMENT;
+    if ((s = check_device()) != LLMINT8_OK) return s;
+    hipError_t e = llmint8::launch_quantize_weight_block(W, dtype == LLMINT8_BF16, batch, (int)N, (int)K, CB, SCB,
+                                                         stream);
+    return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
+}
+
+llmint8_status llmint8_quantize_act_fp8_block(const void* X, int dtype, int64_t M, int64_t K, uint8_t* CA,
+                                              float* SCA, hipStream_t stream) {
+    llmint8_status s = check_dtype(dtype);
+    if (s != LLMINT8_OK) return s;
+    if ((s = check_sizes(M, 0, K)) != LLMINT8_OK) return s;
+    if (M == 0) return LLMINT8_OK;
+    if (bad_ptr(X) || bad_ptr(CA) || bad_ptr(SCA)) return LLMINT8_ERR_INVALID_ARGUMENT;
+    if ((s = check_device()) != LLMINT8_OK) return s;
+    hipError_t e = llmint8::launch_quantize_act_block(X, dtype == LLMINT8_BF16, (int)M, (int)K, CA, SCA, stream);
+    return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
+}
+
+size_t llmint8_matmul_fp8_block_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (check_block_sizes(M, N, K) != LLMINT8_OK) return 0;
+    return llmint8::gemm_block_workspace(M, N, K);
+}
+
+llmint8_status llmint8_matmul_fp8_block(int dtype, int64_t M, int64_t N, int64_t K, const uint8_t* CA,
+                                        const float* SCA, const uint8_t* CB, const float* SCB, const void* bias,
+                                        void* Y, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    llmint8_status s = check_dtype(dtype);
+    if (s != LLMINT8_OK) return s;
+    if ((s = check_block_sizes(M, N, K)) != LLMINT8_OK) return s;
+    if (M == 0 || N == 0) return LLMINT8_OK;
+    if (bad_ptr(CA) || bad_ptr(SCA) || bad_ptr(CB) || bad_ptr(SCB) || bad_ptr(Y) || (bias && !aligned16(bias)))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    if (short_workspace(workspace, workspace_bytes, llmint8::gemm_block_workspace(M, N, K)))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    if ((s = check_device()) != LLMINT8_OK) return s;
+    llmint8::BlockGemmArgs a = block_gemm_args(dtype, M, N, K, CB, SCB, bias, Y);
+    a.CA = CA;
+    a.SCA = SCA;
+    hipError_t e = llmint8::launch_gemm_block(a, workspace, stream);
+    return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
+}
+
+size_t llmint8_linear_fp8_block_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (check_block_sizes(M, N, K) != LLMINT8_OK || M == 0 || N == 0) return 0;
+    return block_act_layout(M, K).end + llmint8::gemm_block_workspace(M, N, K);
+}
+
+llmint8_status llmint8_linear_fp8_block(const void* X, int dtype, int64_t M, int64_t N, int64_t K,
+                                        const uint8_t* CB, const float* SCB, const void* bias, void* Y,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    llmint8_status s = check_dtype(dtype);
+    if (s != LLMINT8_OK) return s;
+    if ((s = check_block_sizes(M, N, K)) != LLMINT8_OK) return s;
+    if (M == 0 || N == 0) return LLMINT8_OK;
+    if (bad_ptr(X) || bad_ptr(CB) || bad_ptr(SCB) || bad_ptr(Y) || (bias && !aligned16(bias)))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    if (short_workspace(workspace, workspace_bytes, llmint8_linear_fp8_block_workspace_size(M, N, K)))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    if ((s = check_device()) != LLMINT8_OK) return s;
+    llmint8::BlockGemmArgs a = block_gemm_args(dtype, M, N, K, CB, SCB, bias, Y);
+    const BlockActLayout L = block_act_layout(M, K);
+    char* ws = static_cast<char*>(workspace);
+    uint8_t* ca = reinterpret_cast<uint8_t*>(ws);
+    float* sca = reinterpret_cast<float*>(ws + L.sca);
+    hipError_t e = llmint8::launch_quantize_act_block(X, a.bf16, a.M, a.K, ca, sca, stream);
+    if (e != hipSuccess) return hip_fail(e);
+    a.CA = ca;
+    a.SCA = sca;
+    e = llmint8::launch_gemm_block(a, ws + L.end, stream);
+    return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
+}
+
+llmint8_status llmint8_route_experts(const void* logits, int logits_dtype, int64_t T, int64_t E, const float* bias,
+                                     int scoring, int n_group, int topk_group, int top_k, int renormalize,
+                                     float scale, int32_t* ids, float* weights, hipStream_t stream) {
+    if (logits_dtype < LLMINT8_F16 || logits_dtype > LLMINT8_F32) return LLMINT8_ERR_INVALID_ARGUMENT;
+    if (scoring != LLMINT8_SOFTMAX && scoring != LLMINT8_SIGMOID) return LLMINT8_ERR_INVALID_ARGUMENT;
+    if (T < 0 || E < 1 || n_group < 1 || E % n_group != 0 || topk_group < 1 || topk_group > n_group || top_k < 1 ||
+        top_k > topk_group * (E / n_group))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    if (T > kMaxDim || E > LLMINT8_EXPERTS_MAX || top_k > LLMINT8_TOP_K_MAX || n_group > LLMINT8_GROUPS_MAX)
+        return LLMINT8_ERR_UNSUPPORTED;
+    if (T == 0) return LLMINT8_OK;
+    if (bad_ptr(logits) || bad_ptr(ids) || bad_ptr(weights) || (bias && !aligned16(bias)))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    llmint8_status s = check_device();
+    if (s != LLMINT8_OK) return s;
+    llmint8::RouteArgs a;
+    a.logits = logits;
+    a.T = T;
+    a.E = (int)E;
+    a.bias = bias;
+    a.sigmoid = scoring == LLMINT8_SIGMOID;
+    a.renormalize = renormalize != 0;
+    a.n_group = n_group;
+    a.topk_group = topk_group;
+    a.top_k = top_k;
+    a.scale = scale;
+    a.ids = ids;
+    a.weights = weights;
+    hipError_t e = llmint8::launch_route(a, logits_dtype, stream);
+    return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
+}
+
+size_t llmint8_experts_fp8_block_workspace_size(int64_t T, int64_t E, int top_k, int64_t K, int64_t I) {
+    if (check_experts(T, E, top_k, K, I) != LLMINT8_OK) return 0;
+    return llmint8::experts_workspace(T, (int)E, top_k, (int)K, (int)I);
+}
+
+llmint8_status llmint8_experts_fp8_block(const void* X, int dtype, int64_t T, int64_t K, int64_t I, int64_t E,
+                                         int top_k, const int32_t* ids, const float* weights, const uint8_t* CB13,
+                                         const float* SCB13, const uint8_t* CB2, const float* SCB2, void* Y,
+                                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    llmint8_status s = check_dtype(dtype);
+    if (s != LLMINT8_OK) return s;
+    if ((s = check_experts(T, E, top_k, K, I)) != LLMINT8_OK) return s;
+    if (T == 0) return LLMINT8_OK;
+    if (bad_ptr(X) || bad_ptr(ids) || bad_ptr(weights) || bad_ptr(CB13) || bad_ptr(SCB13) || bad_ptr(CB2) ||
+        bad_ptr(SCB2) || bad_ptr(Y))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    if (short_workspace(workspace, workspace_bytes,
+                        llmint8::experts_workspace(T, (int)E, top_k, (int)K, (int)I)))
+        return LLMINT8_ERR_INVALID_ARGUMENT;
+    if ((s = check_device()) != LLMINT8_OK) return s;
+    llmint8::ExpertsArgs a;
+    a.X = static_cast<const uint16_t*>(X);
+    a.bf16 = dtype == LLMINT8_BF16;
+    a.T = T;
+    a.K = (int)K;
+    a.I = (int)I;
+    a.E = (int)E;
+    a.top_k = top_k;
+    a.ids = ids;
+    a.weights = weights;
+    a.CB13 = CB13;
+    a.SCB13 = SCB13;
+    a.CB2 = CB2;
+    a.SCB2 = SCB2;
+    a.Y = static_cast<uint16_t*>(Y);
+    hipError_t e = llmint8::launch_experts(a, workspace, stream);
+    return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
 }
 
 llmint8_status llmint8_peak_mfma(int fp8, const int8_t* operands, size_t operand_bytes,

@@ -464,6 +464,18 @@ __device__ __forceinline__ void lds_store(void* base, uint32_t byte_off, T v) {
     *(__attribute__((address_space(3))) T*)((lds_ptr)base + byte_off) = v;
 }
 
+// ---- block-scaled FP8 ---------------------------------------------------------
+// One scale per kBlock consecutive features of an activation row, and per
+// kBlock x kBlock block of a weight.
+constexpr int kBlock = 128;
+
+// The factor of a block's codes from its largest magnitude: 448 / a, held at the
+// largest finite value where the quotient passes it (a < 1.4e-36: the codes then
+// come out smaller than the format allows, but finite).
+__device__ __forceinline__ float block_factor(float a) {
+    return a == 0.0f ? 0.0f : fminf(448.0f / a, 3.402823466e38f);
+}
+
 // ---- launchers (each returns hipGetLastError() after its launches) --------
 // fp8: E4M3 codes (scale 448/absmax) instead of int8 (127/absmax)
 hipError_t launch_quantize_weight(const void* W, bool bf16, bool fp8, int N, int K, int8_t* CB,
@@ -549,6 +561,71 @@ hipError_t launch_linear_decode(const void* X, bool bf16, bool fp8, int M, int N
                                 int8_t* CA, float* SCA, int32_t* idx, int32_t* n_out, void* XO,
                                 int32_t* C_i32, float* C_f32, hipStream_t stream,
                                 hipEvent_t ev_start, hipEvent_t ev_stop);
+
+// ---- block-scaled FP8 launchers ------------------------------------------------
+hipError_t launch_quantize_act_block(const void* X, bool bf16, int M, int K, uint8_t* CA, float* SCA,
+                                     hipStream_t stream);
+hipError_t launch_quantize_weight_block(const void* W, bool bf16, int64_t batch, int N, int K, uint8_t* CB,
+                                        float* SCB, hipStream_t stream);
+
+struct RouteArgs {
+    const void* logits;
+    int64_t T;
+    int E;
+    const float* bias;  // or null
+    bool sigmoid, renormalize;
+    int n_group, topk_group, top_k;
+    float scale;
+    int32_t* ids;
+    float* weights;
+    int group_lanes = 0;  // set by the launcher: lanes that share a group's ranking
+};
+hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t stream);
+
+// A block-scaled product (gemm_block.hip): activation codes CA [M,K] with
+// scales SCA [ceil(K/128)] rows of ld_sa floats, weight codes CB [N,K] with
+// SCB [ceil(N/128), ceil(K/128)].  Dense: Y (+ bias).  Grouped by expert: the
+// tile list `tiles` (count, 3 words unused, then {expert, first row, rows, -}
+// each) and one [N,K] weight per expert, or [2,N,K] for gate and up, whose
+// rows are gathered by row_token and whose result goes to H / SH.
+struct BlockGemmArgs {
+    bool bf16 = false;
+    const uint8_t* CA = nullptr;
+    const float* SCA = nullptr;
+    int64_t ld_sa = 0;
+    const uint8_t* CB = nullptr;
+    const float* SCB = nullptr;
+    int M = 0, N = 0, K = 0;
+    const uint16_t* bias = nullptr;
+    uint16_t* Y = nullptr;
+    const int32_t* tiles = nullptr;
+    const int32_t* row_token = nullptr;
+    uint8_t* H = nullptr;
+    float* SH = nullptr;
+    int64_t ld_sh = 0;
+    float* part = nullptr;
+};
+size_t gemm_block_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, hipStream_t stream);
+int grouped_tile_rows(int64_t pairs, int E);
+hipError_t launch_experts_gate_up(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream);
+hipError_t launch_experts_down(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream);
+
+struct ExpertsArgs {
+    const uint16_t* X;
+    bool bf16;
+    int64_t T;
+    int K, I, E, top_k;
+    const int32_t* ids;
+    const float* weights;
+    const uint8_t* CB13;
+    const float* SCB13;
+    const uint8_t* CB2;
+    const float* SCB2;
+    uint16_t* Y;
+};
+size_t experts_workspace(int64_t T, int E, int top_k, int K, int I);
+hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t stream);
 
 // Kernel families used by launch_matmul.
 constexpr int kSmallM = 16;  // M <= kSmallM takes the streaming kernel

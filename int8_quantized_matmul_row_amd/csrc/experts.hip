@@ -1,0 +1,208 @@
+// The experts' part of a mixture's feed-forward block, around the grouped
+// products of gemm_block.hip: sorting the (token, slot) pairs by expert, and
+// the weighted sum of a token's rows.
+#include "common.h"
+
+namespace llmint8 {
+
+namespace {
+
+constexpr int kSortThreads = 1024;
+constexpr int kMaxExperts = 1024;
+
+// Exclusive prefix sum over kSortThreads values, one per thread; `waves` holds
+// the waves' sums.
+__device__ __forceinline__ int block_excl_scan(int v, int* waves, int* total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int incl = wave_incl_scan(v);
+    __syncthreads();
+    if (lane == 63) waves[wave] = incl;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSortThreads / 64; ++w) {
+        before += w < wave ? waves[w] : 0;
+        all += waves[w];
+    }
+    *total = all;
+    return before + incl - v;
+}
+
+// One workgroup: counts the pairs of each expert, lays the experts' rows out
+// one after another, gives every pair its row (in no particular order within
+// an expert: a row's results do not depend on its place) and lists the tiles
+// of `tile_rows` rows.  Pairs whose id is outside [0, E) get row -1.
+__global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
+                                                                  int top_k, int E, int tile_rows,
+                                                                  int32_t* __restrict__ pair_row,
+                                                                  int32_t* __restrict__ row_token,
+                                                                  int32_t* __restrict__ tiles) {
+    __shared__ int count[kMaxExperts], next[kMaxExperts], waves[kSortThreads / 64];
+    const int tid = threadIdx.x;
+    count[tid] = 0;
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kSortThreads) {
+        const int e = ids[p];
+        if ((uint32_t)e < (uint32_t)E) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    const int c = count[tid];
+    int total;
+    const int first = block_excl_scan(c, waves, &total);
+    next[tid] = first;
+    const int nt = (c + tile_rows - 1) / tile_rows;
+    const int t0 = block_excl_scan(nt, waves, &total);
+    if (tid == 0) tiles[0] = total;
+    for (int t = 0; t < nt; ++t) {
+        int32_t* out = tiles + 4 + 4 * (t0 + t);
+        out[0] = tid;
+        out[1] = first + t * tile_rows;
+        out[2] = min(tile_rows, c - t * tile_rows);
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kSortThreads) {
+        const int e = ids[p];
+        int row = -1;
+        if ((uint32_t)e < (uint32_t)E) {
+            row = atomicAdd(&next[e], 1);
+            row_token[row] = p / top_k;
+        }
+        pair_row[p] = row;
+    }
+}
+
+// Y[t, :] = sum_j w[t, j] * part[row(t, j), :], in fp32 and in the order of j,
+// rounded once.  A thread holds 4 columns of one token.
+template <bool BF16>
+__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part,
+                                                      const int32_t* __restrict__ pair_row,
+                                                      const float* __restrict__ weights, int T, int K, int top_k,
+                                                      uint16_t* __restrict__ Y) {
+    const int64_t quads = (int64_t)T * (K >> 2);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / (K >> 2);
+        const int c = (int)(i - t * (K >> 2)) * 4;
+        v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < top_k; ++j) {
+            const int row = pair_row[t * top_k + j];
+            if (row < 0) continue;
+            const float w = weights[t * top_k + j];
+            const v4f v = *reinterpret_cast<const v4f*>(part + (size_t)row * K + c);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(w, v[q], y[q]);
+        }
+        *reinterpret_cast<uint2*>(Y + t * K + c) =
+            make_uint2(narrow16<BF16>(y[0]) | (uint32_t)narrow16<BF16>(y[1]) << 16,
+                       narrow16<BF16>(y[2]) | (uint32_t)narrow16<BF16>(y[3]) << 16);
+    }
+}
+
+// A chunk of tokens and its share of the workspace.
+struct ExpertsLayout {
+    int64_t tokens;  // of a chunk
+    size_t ca, sca, pair_row, row_token, tiles, h, sh, part, total;
+};
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int64_t max_tiles(int64_t pairs, int E, int tile_rows) {
+    return pairs / tile_rows + (pairs < E ? pairs : E);
+}
+
+// The tokens run in chunks that keep the gathered codes within 32-bit offsets
+// and the rows' intermediate results within kChunkBytes.
+constexpr int64_t kChunkBytes = (int64_t)1 << 30;
+
+ExpertsLayout layout(int64_t T, int E, int top_k, int K, int I) {
+    ExpertsLayout L;
+    int64_t most = kChunkBytes / ((int64_t)top_k * K * 4);
+    if (most > 0xf0000000ll / K) most = 0xf0000000ll / K;
+    if (most < 1) most = 1;
+    L.tokens = T < most ? T : most;
+    const int64_t n = L.tokens, P = n * top_k;
+    const int nkb = (K + kBlock - 1) / kBlock, nib = (I + kBlock - 1) / kBlock;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += up256(bytes);
+        return was;
+    };
+    L.ca = take((size_t)n * K);
+    L.sca = take((size_t)nkb * n * 4);
+    L.pair_row = take((size_t)P * 4);
+    L.row_token = take((size_t)P * 4);
+    L.tiles = take(16 + 16 * (size_t)max_tiles(P, E, 32));
+    L.h = take((size_t)P * I);
+    L.sh = take((size_t)nib * P * 4);
+    L.part = take((size_t)P * K * 4);
+    L.total = at;
+    return L;
+}
+
+}  // namespace
+
+size_t experts_workspace(int64_t T, int E, int top_k, int K, int I) {
+    return T == 0 ? 0 : layout(T, E, top_k, K, I).total;
+}
+
+hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t stream) {
+    const ExpertsLayout L = layout(a.T, a.E, a.top_k, a.K, a.I);
+    char* ws = static_cast<char*>(workspace);
+    for (int64_t t0 = 0; t0 < a.T; t0 += L.tokens) {
+        const int n = (int)(a.T - t0 < L.tokens ? a.T - t0 : L.tokens);
+        const int P = n * a.top_k;
+        const int tile_rows = grouped_tile_rows(P, a.E);
+        uint8_t* ca = reinterpret_cast<uint8_t*>(ws + L.ca);
+        float* sca = reinterpret_cast<float*>(ws + L.sca);
+        int32_t* pair_row = reinterpret_cast<int32_t*>(ws + L.pair_row);
+        int32_t* row_token = reinterpret_cast<int32_t*>(ws + L.row_token);
+        int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
+        uint8_t* h = reinterpret_cast<uint8_t*>(ws + L.h);
+        float* sh = reinterpret_cast<float*>(ws + L.sh);
+        float* part = reinterpret_cast<float*>(ws + L.part);
+        hipError_t e = launch_quantize_act_block(a.X + (size_t)t0 * a.K, a.bf16, n, a.K, ca, sca, stream);
+        if (e != hipSuccess) return e;
+        sort_pairs_kernel<<<1, kSortThreads, 0, stream>>>(a.ids + t0 * a.top_k, P, a.top_k, a.E, tile_rows, pair_row,
+                                                          row_token, tiles);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        BlockGemmArgs g;
+        g.bf16 = a.bf16;
+        g.CA = ca;
+        g.SCA = sca;
+        g.ld_sa = n;
+        g.CB = a.CB13;
+        g.SCB = a.SCB13;
+        g.M = n;
+        g.N = a.I;
+        g.K = a.K;
+        g.tiles = tiles;
+        g.row_token = row_token;
+        g.H = h;
+        g.SH = sh;
+        g.ld_sh = P;
+        const int64_t mt = max_tiles(P, a.E, tile_rows);
+        if ((e = launch_experts_gate_up(g, tile_rows, mt, stream)) != hipSuccess) return e;
+        g.CA = h;
+        g.SCA = sh;
+        g.ld_sa = P;
+        g.CB = a.CB2;
+        g.SCB = a.SCB2;
+        g.M = P;
+        g.N = a.K;
+        g.K = a.I;
+        g.part = part;
+        if ((e = launch_experts_down(g, tile_rows, mt, stream)) != hipSuccess) return e;
+        const int64_t blocks = ((int64_t)n * (a.K / 4) + 255) / 256;
+        const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
+        uint16_t* y = a.Y + (size_t)t0 * a.K;
+        const float* w = a.weights + t0 * a.top_k;
+        if (a.bf16)
+            combine_kernel<true><<<grid, 256, 0, stream>>>(part, pair_row, w, n, a.K, a.top_k, y);
+        else
+            combine_kernel<false><<<grid, 256, 0, stream>>>(part, pair_row, w, n, a.K, a.top_k, y);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace llmint8

@@ -1,0 +1,399 @@
+// Block-scaled FP8 product on tiles:
+//   Y[m,n] = sum_b SCA[b,m] SCB[n/128,b] / 448^2 * (sum_{k in block b} CA[m,k] CB[n,k]),
+// as a dense product (+ bias, 16-bit Y), and over rows grouped by expert for
+// the two products of a mixture's feed-forward block:
+//   kGateUp  rows gathered from the tokens' codes, weight rows n and I + n
+//            (gate and up) side by side in one tile; h = silu(g) * u leaves
+//            the tile as E4M3 codes with one scale per 128 channels;
+//   kDown    h's codes against the down weights, fp32 rows out (a later
+//            kernel weights and sums a token's rows).
+//
+// One v_mfma_f32_16x16x128_f8f6f4 covers a whole scale block of K, from a zero
+// accumulator; its 16 x 16 result is then added into fp32 registers times the
+// block's scale, SCA * SCB, by ordinary fused multiply-adds.  The weight is
+// the MFMA's first operand, so that a lane's four results belong to one token
+// row (one scale) and four consecutive channels.
+//
+// A tile's K stages are 128 bytes of every row, in a ring of two LDS buffers
+// filled by buffer loads that go straight to LDS; 16-byte chunk c of row r
+// sits in slot c ^ ((r / 2) % 8), so 16 rows' fragment reads cover the banks
+// evenly.  Stage kt + 1 loads while stage kt is multiplied.
+#include "common.h"
+
+namespace llmint8 {
+
+namespace {
+
+constexpr int kStageK = kBlock;  // bytes of K per stage: one scale block
+constexpr int kMaxKb = (LLMINT8_K_MAX + kBlock - 1) / kBlock;
+constexpr float kCodeScale = 1.0f / (448.0f * 448.0f);
+constexpr int64_t kMaxGrid = 0x7fffff;  // workgroups of up to 512 threads: below 2^32 threads
+constexpr uint32_t kPastEnd = 0xffffff00u;  // a buffer offset that reads 0
+
+enum BlockMode { kDense, kGateUp, kDown };
+
+__device__ __forceinline__ v4f mfma_block(const v8i& w, const v8i& x) {
+    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// lane p's 4 bytes at gptr land in LDS at lds_addr + 4 p
+__device__ __forceinline__ void dma4(const float* gptr, uint32_t lds_addr) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %2, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(lds_addr), "v"(gptr)
+        : "memory");
+}
+
+// Workgroups go round-robin over the 8 XCDs: block b of `total` becomes place
+// L of an order in which each XCD walks a contiguous range.
+__device__ __forceinline__ int xcd_order(int b, int total) {
+    const int q = total >> 3, r = total & 7, x = b & 7;
+    return x * q + min(x, r) + (b >> 3);
+}
+
+template <int BM_, int WM_, int WN_>
+struct Shape {
+    static constexpr int BM = BM_, BN = 256, WM = WM_, WN = WN_, NW = WM * WN;
+    static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;  // 16 x 16 tiles of a wave
+    static constexpr int kStageBytes = (BM + BN) * kStageK;
+    static constexpr int kSa = BM < 64 ? 64 : BM;  // floats of a stage's row scales
+    static constexpr int kDmaA = BM / 8 / NW, kDmaB = BN / 8 / NW;
+    static_assert(kDmaA * 8 * NW == BM && kDmaB * 8 * NW == BN, "whole loads per wave");
+    static_assert(NT * 16 * WN == BN && MT * 16 * WM == BM, "whole tiles per wave");
+};
+
+template <typename S, int MODE, bool BF16>
+__global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a) {
+    __shared__ __align__(1024) int8_t ring[2 * S::kStageBytes];
+    __shared__ float s_sa[2 * S::kSa];
+    __shared__ float s_sb[2 * kMaxKb];
+    constexpr int BM = S::BM, BN = S::BN, MT = S::MT, NT = S::NT;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    const int K = a.K, nkb = (K + kBlock - 1) / kBlock;
+    const int chans = MODE == kGateUp ? BN / 2 : BN;  // output channels of a tile
+    const int tiles_n = (a.N + chans - 1) / chans;
+
+    // ---- which tile: rows [row0, row0 + rows) of the (sorted) activations,
+    // channels from n0 of weight matrix `e`
+    int row0, rows, n0, e = 0;
+    if constexpr (MODE == kDense) {
+        constexpr int kGroupM = 4;  // tile rows that share a weight panel in L2
+        const int tiles_m = (int)(((int64_t)a.M + BM - 1) / BM);
+        const int L = xcd_order(blockIdx.x, tiles_m * tiles_n);
+        const int first = L / (kGroupM * tiles_n) * kGroupM;
+        const int gsz = min(tiles_m - first, kGroupM), in = L - first * tiles_n;
+        row0 = (first + in % gsz) * BM;
+        n0 = in / gsz * chans;
+        rows = min(BM, a.M - row0);
+    } else {
+        const int total = a.tiles[0] * tiles_n;
+        if ((int)blockIdx.x >= total) return;
+        const int L = xcd_order(blockIdx.x, total);
+        const int32_t* t = a.tiles + 4 + 4 * (L / tiles_n);
+        e = __builtin_amdgcn_readfirstlane(t[0]);
+        row0 = __builtin_amdgcn_readfirstlane(t[1]);
+        rows = __builtin_amdgcn_readfirstlane(t[2]);
+        n0 = L % tiles_n * chans;
+    }
+
+    // ---- weight block scales of the tile's two 128-channel halves (gate and
+    // up, or channels n0.. and n0 + 128..), with the codes' 1/448^2
+    const int nnb = (a.N + kBlock - 1) / kBlock;
+    {
+        const float* sb0;
+        const float* sb1;
+        if constexpr (MODE == kGateUp) {
+            sb0 = a.SCB + ((size_t)e * 2 * nnb + n0 / kBlock) * nkb;
+            sb1 = sb0 + (size_t)nnb * nkb;
+        } else {
+            sb0 = a.SCB + ((size_t)e * nnb + n0 / kBlock) * nkb;
+            sb1 = n0 + kBlock < a.N ? sb0 + nkb : sb0;
+        }
+        for (int i = tid; i < nkb; i += 64 * S::NW) {
+            s_sb[i] = sb0[i] * kCodeScale;
+            s_sb[kMaxKb + i] = sb1[i] * kCodeScale;
+        }
+    }
+
+    // ---- stage loads: one instruction = 8 rows x 128 bytes; lane p fills slot
+    // p % 8 of row p / 8 and so fetches logical chunk (p % 8) ^ ((row / 2) % 8).
+    // Rows past the tile's re-read a valid row (their results are never stored).
+    const uint8_t* base_a = a.CA;
+    const uint8_t* base_b;
+    uint32_t bytes_a, bytes_b;
+    if constexpr (MODE == kGateUp) {
+        bytes_a = (uint32_t)((int64_t)a.M * K);  // gathered rows (below 2^32 bytes in all)
+        base_b = a.CB + (size_t)e * 2 * a.N * K;
+        bytes_b = (uint32_t)((int64_t)2 * a.N * K);
+    } else {
+        base_a += (size_t)row0 * K;
+        bytes_a = (uint32_t)rows * (uint32_t)K;
+        base_b = a.CB + ((size_t)e * a.N + n0) * K;
+        bytes_b = (uint32_t)min(BN, a.N - n0) * (uint32_t)K;
+    }
+    const v4i rsrc_a = buffer_rsrc(base_a, bytes_a), rsrc_b = buffer_rsrc(base_b, bytes_b);
+    uint32_t voff_a[S::kDmaA], voff_b[S::kDmaB];
+    const int ch = ((lane & 7) ^ ((lane >> 4) & 3)) * 16;  // for even 8-row groups; odd ones flip bit 2
+    // byte of the row where this lane's chunk starts, for the 8-row group `grp`
+    auto chunk = [&](int grp) { return (grp & 1) ? ch ^ 64 : ch; };
+#pragma unroll
+    for (int i = 0; i < S::kDmaA; ++i) {
+        const int grp = S::kDmaA * wave + i, r = min(8 * grp + (lane >> 3), rows - 1);
+        uint32_t row = (uint32_t)r;
+        if constexpr (MODE == kGateUp) row = (uint32_t)a.row_token[row0 + r];
+        voff_a[i] = row * (uint32_t)K + chunk(grp);
+    }
+#pragma unroll
+    for (int i = 0; i < S::kDmaB; ++i) {
+        const int grp = S::kDmaB * wave + i, r = 8 * grp + (lane >> 3);
+        uint32_t row;
+        if constexpr (MODE == kGateUp) {
+            // a wave's 64 rows: gate of its 32 channels, then up of the same
+            const int c = min(n0 + (r >> 6) * 32 + (r & 31), a.N - 1);
+            row = (uint32_t)(c + ((r >> 5) & 1) * a.N);
+        } else {
+            row = (uint32_t)min(r, a.N - n0 - 1);
+        }
+        voff_b[i] = row * (uint32_t)K + chunk(grp);
+    }
+    // the row scales: lane p of each instruction one row of 64
+    const float* sa_ptr;
+    {
+        const int r = min((64 * wave + lane) % S::kSa, rows - 1);
+        if constexpr (MODE == kGateUp)
+            sa_ptr = a.SCA + a.row_token[row0 + r];
+        else
+            sa_ptr = a.SCA + row0 + r;
+    }
+    const uint32_t lds_ring = lds_address(ring);
+    const uint32_t lds_sa = lds_address(reinterpret_cast<const int8_t*>(s_sa)) + (64 * wave % S::kSa) * 4;
+    const int half_kt = K % kStageK != 0 ? nkb - 1 : -1;  // the stage whose second half is past K
+    auto dma = [&](int kt, int u) {
+        const uint32_t kd = (uint32_t)kt * kStageK;
+#pragma unroll
+        for (int i = 0; i < S::kDmaA; ++i) {
+            const int grp = S::kDmaA * wave + i;
+            const uint32_t off = kt == half_kt && chunk(grp) >= 64 ? kPastEnd : voff_a[i] + kd;
+            dma_line(rsrc_a, off, lds_ring + u * S::kStageBytes + grp * 8 * kStageK);
+        }
+#pragma unroll
+        for (int i = 0; i < S::kDmaB; ++i) {
+            const int grp = S::kDmaB * wave + i;
+            const uint32_t off = kt == half_kt && chunk(grp) >= 64 ? kPastEnd : voff_b[i] + kd;
+            dma_line(rsrc_b, off, lds_ring + u * S::kStageBytes + (BM + grp * 8) * kStageK);
+        }
+        dma4(sa_ptr + (int64_t)kt * a.ld_sa, lds_sa + u * S::kSa * 4);
+    };
+
+    // ---- fragments: lane l holds 32 bytes of row (l % 16), chunks l / 16 and
+    // l / 16 + 4 (the same K order for both operands)
+    const int fr = lane & 15;
+    const uint32_t f_lo = fr * kStageK + (((lane >> 4) ^ (fr >> 1)) & 7) * 16, f_hi = f_lo ^ 64;
+    auto frag = [&](int u, int row) -> v8i {
+        const uint32_t at = u * S::kStageBytes + row * kStageK;
+        const v4i lo = lds_load<v4i>(ring, at + f_lo), hi = lds_load<v4i>(ring, at + f_hi);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+
+    v4f acc[NT][MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kWaveM = MT * 16, kWaveN = NT * 16;
+    // which half's weight scale a wave's channel tiles take
+    const int half_of_wave = MODE == kGateUp ? 0 : wn * kWaveN / kBlock;
+
+    auto stage = [&](int kt, int u) {
+        wait_vmcnt<0>();
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS reads and writes are done
+        stage_barrier();
+        if (kt + 1 < nkb) dma(kt + 1, 1 - u);
+        const float sb0 = s_sb[half_of_wave * kMaxKb + kt];
+        const float sb1 = MODE == kGateUp ? s_sb[kMaxKb + kt] : sb0;
+        v8i w[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) w[i] = frag(u, BM + wn * kWaveN + 16 * i);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const v8i x = frag(u, wm * kWaveM + 16 * j);
+            const float sa = s_sa[u * S::kSa + wm * kWaveM + 16 * j + fr];
+            const float f0 = sa * sb0, f1 = MODE == kGateUp ? sa * sb1 : f0;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const v4f p = mfma_block(w[i], x);
+                const float f = MODE == kGateUp && i >= NT / 2 ? f1 : f0;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], f, acc[i][j][v]);
+            }
+        }
+    };
+    dma(0, 0);
+    int kt = 0;
+    for (; kt + 2 <= nkb; kt += 2) {
+        stage(kt, 0);
+        stage(kt + 1, 1);
+    }
+    if (kt < nkb) stage(kt, 0);
+
+    // ---- results: lane l holds channels 4 (l / 16) .. + 3 of each 16-channel
+    // tile for token row l % 16 of each 16-row tile
+    const int cq = (lane >> 4) * 4;
+    if constexpr (MODE == kDense) {
+        uint16_t* Y = a.Y + (size_t)row0 * a.N;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int n = n0 + wn * kWaveN + 16 * i + cq;
+            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (a.bias != nullptr)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (n + v < a.N) b[v] = widen16<BF16>(a.bias[n + v]);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const int m = wm * kWaveM + 16 * j + fr;
+                if (m >= rows) continue;
+                uint16_t y[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y[v] = narrow16<BF16>(acc[i][j][v] + b[v]);
+                uint16_t* out = Y + (size_t)m * a.N + n;
+                if ((a.N & 3) == 0 && n < a.N) {
+                    *reinterpret_cast<uint2*>(out) = make_uint2(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (n + v < a.N) out[v] = y[v];
+                }
+            }
+        }
+    } else if constexpr (MODE == kDown) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int n = n0 + wn * kWaveN + 16 * i + cq;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const int m = wm * kWaveM + 16 * j + fr;
+                if (m < rows && n < a.N)  // (N is a multiple of 64)
+                    *reinterpret_cast<v4f*>(a.part + (size_t)(row0 + m) * a.N + n) = acc[i][j];
+            }
+        }
+    } else {
+        // h of 32 channels per wave; a row's maximum over the tile's 128
+        // channels from the four waves that share its rows
+        static_assert(MODE != kGateUp || (NT == 4 && S::WN == 4), "gate and up of 32 channels per wave");
+        float* red = reinterpret_cast<float*>(ring);  // [WN][BM]
+        stage_barrier();  // every wave is done with the ring (its own reads have returned)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i) {
+                const bool in = n0 + wn * 32 + 16 * i + cq < a.N;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float g = acc[i][j][v], u = acc[i + NT / 2][j][v];
+                    const float h = in ? g / (1.0f + expf(-g)) * u : 0.0f;
+                    acc[i][j][v] = h;
+                    m = fmaxf(m, fabsf(h));
+                }
+            }
+            m = fmaxf(m, __shfl_xor(m, 16));
+            m = fmaxf(m, __shfl_xor(m, 32));
+            if (lane < 16) red[wn * BM + wm * kWaveM + 16 * j + lane] = m;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int r = wm * kWaveM + 16 * j + fr;
+            const float m = fmaxf(fmaxf(red[r], red[BM + r]), fmaxf(red[2 * BM + r], red[3 * BM + r]));
+            const float f = block_factor(m);
+            if (r >= rows) continue;
+            if (wn == 0 && lane < 16) a.SH[(int64_t)(n0 / kBlock) * a.ld_sh + row0 + r] = m;
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i) {
+                const int n = n0 + wn * 32 + 16 * i + cq;
+                if (n < a.N)
+                    *reinterpret_cast<uint32_t*>(a.H + (size_t)(row0 + r) * a.N + n) =
+                        e4m3_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], f);
+            }
+        }
+    }
+}
+
+typedef Shape<256, 2, 4> Tile256;
+typedef Shape<128, 2, 4> Tile128;
+typedef Shape<32, 1, 4> Tile32;
+
+template <typename S, int MODE>
+hipError_t launch(const BlockGemmArgs& a, int64_t tiles_m, hipStream_t stream) {
+    const int chans = MODE == kGateUp ? S::BN / 2 : S::BN;
+    const int64_t grid = tiles_m * ((a.N + chans - 1) / chans);
+    if (grid > kMaxGrid) return hipErrorInvalidValue;
+    if (a.bf16 && MODE == kDense)
+        gemm_block_kernel<S, MODE, true><<<dim3((unsigned)grid), 64 * S::NW, 0, stream>>>(a);
+    else
+        gemm_block_kernel<S, MODE, false><<<dim3((unsigned)grid), 64 * S::NW, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gemm_block_workspace(int64_t, int64_t, int64_t) { return 0; }
+
+namespace {
+
+// Row blocks of the activations small enough for one launch's grid.
+template <typename S>
+hipError_t launch_dense(BlockGemmArgs a, hipStream_t stream) {
+    const int64_t tiles_n = ((int64_t)a.N + S::BN - 1) / S::BN;
+    const int64_t most = kMaxGrid / tiles_n * S::BM, all = a.M;
+    const uint8_t* CA = a.CA;
+    const float* SCA = a.SCA;
+    uint16_t* Y = a.Y;
+    for (int64_t m = 0; m < all; m += most) {
+        a.M = (int)(all - m < most ? all - m : most);
+        a.CA = CA + m * a.K;
+        a.SCA = SCA + m;
+        a.Y = Y + m * a.N;
+        const hipError_t e = launch<S, kDense>(a, ((int64_t)a.M + S::BM - 1) / S::BM, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, hipStream_t stream) {
+    (void)workspace;
+    if (a.M > 512) return launch_dense<Tile256>(a, stream);
+    if (a.M > 64) return launch_dense<Tile128>(a, stream);
+    return launch_dense<Tile32>(a, stream);
+}
+
+int grouped_tile_rows(int64_t pairs, int E) {
+    const int64_t mean = pairs / E;
+    return mean > 256 ? 256 : mean > 48 ? 128 : 32;
+}
+
+hipError_t launch_experts_gate_up(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
+    if (tile_rows == 256) return launch<Tile256, kGateUp>(a, max_tiles, stream);
+    if (tile_rows == 128) return launch<Tile128, kGateUp>(a, max_tiles, stream);
+    return launch<Tile32, kGateUp>(a, max_tiles, stream);
+}
+
+hipError_t launch_experts_down(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
+    if (tile_rows == 256) return launch<Tile256, kDown>(a, max_tiles, stream);
+    if (tile_rows == 128) return launch<Tile128, kDown>(a, max_tiles, stream);
+    return launch<Tile32, kDown>(a, max_tiles, stream);
+}
+
+}  // namespace llmint8

@@ -1,0 +1,137 @@
+// Quantization to FP8 E4M3 codes with one scale per block: activations in
+// blocks of 128 consecutive features of a token row, weights in blocks of
+// 128 x 128.
+//
+// For a block with largest magnitude a:  code = e4m3(x * (448 / a)), one fp32
+// divide per block and one fp32 multiply per value, rounded to the nearest
+// E4M3 number; a == 0 gives factor 0 (codes of signed zeros), and a quotient past
+// the largest finite value is held there (block_factor).  The scale kept
+// is a itself, so a code stands for value * a / 448.
+#include "common.h"
+
+namespace llmint8 {
+
+// max over the 16 lanes of a row of lanes, returned to all 16
+__device__ __forceinline__ float row16_max(float v) {
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0xB1>(0, __builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x4E>(0, __builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x141>(0, __builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x140>(0, __builtin_bit_cast(int, v))));
+    return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float absmax8(const v8u16& v) {
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(widen16<BF16>(v[e])));
+    return a;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint2 codes8(const v8u16& v, float f) {
+    return make_uint2(e4m3_pack4(widen16<BF16>(v[0]), widen16<BF16>(v[1]), widen16<BF16>(v[2]), widen16<BF16>(v[3]), f),
+                      e4m3_pack4(widen16<BF16>(v[4]), widen16<BF16>(v[5]), widen16<BF16>(v[6]), widen16<BF16>(v[7]), f));
+}
+
+// ---- activations -----------------------------------------------------------
+// 16 lanes hold one block of a row (8 values, one 16-byte load each) and
+// reduce its maximum among themselves; a workgroup of 16 such groups takes 16
+// rows, so the block's scales go out as 16 consecutive floats of the
+// block-major SCA [ceil(K/128), M], and kActBlocks blocks of each row, whose
+// loads are all in flight together.  HBM-bound: 2MK read, MK + 4M ceil(K/128)
+// written.
+constexpr int kActBlocks = 4;
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_act_block_kernel(const uint16_t* __restrict__ X, int M, int K,
+                                                                 uint8_t* __restrict__ CA, float* __restrict__ SCA) {
+    const int grp = threadIdx.x >> 4, q = threadIdx.x & 15;
+    const int nkb = (K + kBlock - 1) / kBlock;
+    const int b0 = blockIdx.y * kActBlocks;
+    for (int64_t m = (int64_t)blockIdx.x * 16 + grp; m < M; m += (int64_t)gridDim.x * 16) {
+        v8u16 v[kActBlocks];
+#pragma unroll
+        for (int i = 0; i < kActBlocks; ++i) {
+            const int c = (b0 + i) * kBlock + 8 * q;
+            v[i] = c < K ? *reinterpret_cast<const v8u16*>(X + m * K + c) : v8u16{0, 0, 0, 0, 0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < kActBlocks; ++i) {
+            const int b = b0 + i, c = b * kBlock + 8 * q;
+            if (b >= nkb) break;
+            const float a = row16_max(absmax8<BF16>(v[i]));
+            const float f = block_factor(a);
+            if (c < K) *reinterpret_cast<uint2*>(CA + m * K + c) = codes8<BF16>(v[i], f);
+            if (q == 0) SCA[(int64_t)b * M + m] = a;
+        }
+    }
+}
+
+hipError_t launch_quantize_act_block(const void* X, bool bf16, int M, int K, uint8_t* CA, float* SCA,
+                                     hipStream_t stream) {
+    const int nkb = (K + kBlock - 1) / kBlock;
+    const int want = M / 16 + (M % 16 != 0);
+    const dim3 grid((unsigned)(want < 65536 ? want : 65536), (unsigned)((nkb + kActBlocks - 1) / kActBlocks));
+    const uint16_t* x = static_cast<const uint16_t*>(X);
+    if (bf16)
+        quantize_act_block_kernel<true><<<grid, 256, 0, stream>>>(x, M, K, CA, SCA);
+    else
+        quantize_act_block_kernel<false><<<grid, 256, 0, stream>>>(x, M, K, CA, SCA);
+    return hipGetLastError();
+}
+
+// ---- weights ---------------------------------------------------------------
+// One workgroup per 128 x 128 block (two rows of lanes per 256 bytes of a
+// weight row, 16 rows at a time): the block stays in registers between the
+// maximum and the codes, so W is read once.  HBM-bound: 2NK read, NK written.
+template <bool BF16>
+__global__ __launch_bounds__(256) void quantize_weight_block_kernel(const uint16_t* __restrict__ W, int N, int K,
+                                                                    uint8_t* __restrict__ CB,
+                                                                    float* __restrict__ SCB) {
+    __shared__ float part[4];
+    const int grp = threadIdx.x >> 4, q = threadIdx.x & 15;
+    const int nkb = (K + kBlock - 1) / kBlock, nnb = (N + kBlock - 1) / kBlock;
+    // a batch's blocks follow one another in blockIdx.x, k fastest
+    const int64_t id = blockIdx.x;
+    const int kb = (int)(id % nkb);
+    const int64_t nb_all = id / nkb;
+    const int nb = (int)(nb_all % nnb);
+    const int64_t batch = nb_all / nnb;
+    const int c = kb * kBlock + 8 * q;
+    const size_t base = (size_t)batch * N * K + c;
+    v8u16 v[8];
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = nb * kBlock + 16 * i + grp;
+        v[i] = n < N && c < K ? *reinterpret_cast<const v8u16*>(W + base + (size_t)n * K)
+                              : v8u16{0, 0, 0, 0, 0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, absmax8<BF16>(v[i]));
+    a = wave_max(a);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+    __syncthreads();
+    a = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    if (threadIdx.x == 0) SCB[id] = a;
+    const float f = block_factor(a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = nb * kBlock + 16 * i + grp;
+        if (n < N && c < K) *reinterpret_cast<uint2*>(CB + base + (size_t)n * K) = codes8<BF16>(v[i], f);
+    }
+}
+
+hipError_t launch_quantize_weight_block(const void* W, bool bf16, int64_t batch, int N, int K, uint8_t* CB,
+                                        float* SCB, hipStream_t stream) {
+    const int64_t blocks = batch * ((N + kBlock - 1) / kBlock) * ((K + kBlock - 1) / kBlock);
+    const uint16_t* w = static_cast<const uint16_t*>(W);
+    if (bf16)
+        quantize_weight_block_kernel<true><<<dim3((unsigned)blocks), 256, 0, stream>>>(w, N, K, CB, SCB);
+    else
+        quantize_weight_block_kernel<false><<<dim3((unsigned)blocks), 256, 0, stream>>>(w, N, K, CB, SCB);
+    return hipGetLastError();
+}
+
+}  // namespace llmint8

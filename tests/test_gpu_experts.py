@@ -1,0 +1,155 @@
+"""GPU parity of the experts' products against a float64 reference.
+
+The reference quantizes X in the library's fp32 arithmetic and h in float64.
+Where the kernel's fp32 h falls on the other side of a rounding point, a code
+moves by a step, which shows in all of a token's outputs.  Two checks:
+  * every element within block_ref.experts' bound, which follows h's own error
+    through the codes it may move, plus the 16-bit type's rounding;
+  * the whole output within a relative 2-norm of 2^-7 plus the type's half step:
+    an h off by 2^-11 moves about 2^-7.5 of its codes, each by 2^-3.5 of the value in
+    the mean, which is 2^(-7.5/2 - 3.5) = 2^-7.25 over all elements.
+"""
+import numpy as np
+import pytest
+
+import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import int8_quantized_matmul_row_amd as pkg
+    pkg.lib()
+
+
+def make(T, E, K, I, dtype, seed):
+    """X, the quantized weights, and their float64 values."""
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    g = torch.Generator().manual_seed(seed)
+    dt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    x = torch.randn(T, K, generator=g).to(dt)
+    w13 = (torch.randn(E, 2, I, K, generator=g) / K ** 0.5 * torch.rand(E, 2, 1, 1, generator=g).add(0.5)).to(dt)
+    w2 = (torch.randn(E, K, I, generator=g) / I ** 0.5).to(dt)
+    q13, q2 = pkg.quantize_weight_fp8_block(w13.cuda()), pkg.quantize_weight_fp8_block(w2.cuda())
+
+    def values(q):
+        codes = q[0].view(torch.float8_e4m3fn).float().cpu().numpy().astype(np.float64)
+        flat, s = codes.reshape(-1, *codes.shape[-2:]), q[1].cpu().numpy().reshape(-1, *q[1].shape[-2:])
+        return np.stack([f * ref.spread(t, 128, *f.shape) for f, t in zip(flat, s)]).reshape(codes.shape)
+
+    codes, scales = ref.quantize(x.float().numpy(), 1)
+    return x.cuda(), q13, q2, codes * ref.spread(scales, 1, T, K), values(q13), values(q2)
+
+
+def close(Y, reference, dtype):
+    want, bound = reference
+    y = Y.float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(y).all()
+    err = np.abs(y - want)
+    worst = (err / (bound + 2 * ref.half_step16(np.abs(want) + bound, dtype == "bf16"))).max()
+    norm, scale = np.linalg.norm(err), np.linalg.norm(want)
+    tol = (2.0 ** -7 + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -11)) * scale + 1e-6
+    print(f"worst error / bound {worst:.3f}, 2-norm / tolerance {norm / tol:.3f}", flush=True)
+    assert worst <= 1.0 and norm <= tol
+
+
+CASES = [(1, 1, 1, 64, 64), (1, 8, 2, 128, 128), (1, 64, 8, 512, 192), (3, 4, 4, 192, 64), (5, 8, 1, 256, 320),
+         (16, 2, 1, 320, 128), (17, 2, 2, 128, 192), (33, 16, 6, 256, 256), (130, 4, 2, 192, 128), (257, 3, 1, 128, 64),
+         (300, 2, 2, 256, 192), (600, 2, 1, 64, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,E,k,K,I", CASES)
+def test_experts(T, E, k, K, I, dtype):
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    x, q13, q2, xv, w13, w2 = make(T, E, K, I, dtype, T + E + K)
+    g = torch.Generator().manual_seed(9)
+    ids = torch.rand(T, E, generator=g).argsort(dim=1)[:, :k].to(torch.int32)
+    weights = torch.rand(T, k, generator=g)
+    Y = pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2)
+    close(Y, ref.experts(xv, ids.numpy(), weights.numpy(), w13, w2), dtype)
+    again = pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2, out=torch.empty_like(Y))
+    assert torch.equal(again, Y)
+
+
+@pytest.mark.parametrize("T", [6, 60, 400])
+def test_uneven_and_dropped(T):
+    """One expert takes most rows, some none; ids of -1, of other ranks, and doubled."""
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    E, k, K, I = 7, 3, 256, 192
+    x, q13, q2, xv, w13, w2 = make(T, E, K, I, "bf16", T)
+    g = torch.Generator().manual_seed(T)
+    ids = torch.full((T, k), 4, dtype=torch.int32)
+    ids[:, 1] = torch.randint(-2, E + 3, (T,), generator=g)
+    ids[:, 2] = torch.where(torch.rand(T, generator=g) < 0.2, 6, -1)
+    ids[T // 2] = torch.tensor([-1, 1 << 30, -(1 << 31)])
+    ids[1] = 2
+    weights = torch.randn(T, k, generator=g)
+    Y = pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2)
+    want = ref.experts(xv, ids.numpy(), weights.numpy(), w13, w2)
+    assert (Y[T // 2] == 0).all()
+    close(Y, want, "bf16")
+
+
+def test_rows_of_tokens_that_no_expert_takes_are_not_read():
+    """A padding token's values (here NaN) reach nobody's output."""
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    x, q13, q2, xv, w13, w2 = make(20, 4, 128, 128, "f16", 3)
+    ids = torch.randint(0, 4, (20, 2), dtype=torch.int32)
+    ids[7:9] = -1
+    weights = torch.full((20, 2), 0.5)
+    want = ref.experts(xv, ids.numpy(), weights.numpy(), w13, w2)
+    x[7:9] = float("nan")
+    Y = pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2)
+    assert (Y[7:9] == 0).all()
+    close(Y, want, "f16")
+
+
+def test_no_tokens():
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    x, q13, q2, *_ = make(4, 2, 128, 64, "f16", 1)
+    Y = pkg.experts_fp8_block(x[:0], torch.zeros(0, 2, dtype=torch.int32, device="cuda"),
+                              torch.zeros(0, 2, device="cuda"), *q13, *q2)
+    assert tuple(Y.shape) == (0, 128)
+
+
+def test_tokens_in_chunks():
+    """More rows than one pass of the workspace holds: the same rows as alone."""
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    T, E, k, K, I = 40000, 2, 2, 4096, 64
+    assert T * k * K * 4 > 1 << 30
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    q13 = pkg.quantize_weight_fp8_block((torch.randn(E, 2, I, K, generator=g, device="cuda") / 64).bfloat16())
+    q2 = pkg.quantize_weight_fp8_block((torch.randn(E, K, I, generator=g, device="cuda") / 8).bfloat16())
+    ids = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    Y = pkg.experts_fp8_block(x, ids, w, *q13, *q2)
+    for at in (slice(0, 600), slice(32700, 33300), slice(T - 600, T)):
+        alone = pkg.experts_fp8_block(x[at].contiguous(), ids[at].contiguous(), w[at].contiguous(), *q13, *q2)
+        assert torch.equal(alone, Y[at])
+
+
+@pytest.mark.parametrize("T", [5, 200])
+def test_another_stream(T):
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    x, q13, q2, *_ = make(T, 4, 256, 128, "bf16", 2)
+    ids = torch.randint(0, 4, (T, 2), dtype=torch.int32).cuda()
+    w = torch.full((T, 2), 0.5).cuda()
+    want = pkg.experts_fp8_block(x, ids, w, *q13, *q2)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [pkg.experts_fp8_block(x, ids, w, *q13, *q2, stream=s) for _ in range(4)]
+    s.synchronize()
+    assert all(torch.equal(y, want) for y in got)
