@@ -459,6 +459,10 @@ __device__ __forceinline__ T lds_load(const void* base, uint32_t byte_off) {
     return *(const __attribute__((address_space(3))) T*)((lds_cptr)base + byte_off);
 }
 template <typename T>
+__device__ __forceinline__ T lds_at(uint32_t addr) {
+    return *(const __attribute__((address_space(3))) T*)addr;
+}
+template <typename T>
 __device__ __forceinline__ void lds_store(void* base, uint32_t byte_off, T v) {
     typedef __attribute__((address_space(3))) char* lds_ptr;
     *(__attribute__((address_space(3))) T*)((lds_ptr)base + byte_off) = v;

@@ -126,7 +126,7 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
 
     // ---- stage loads: one instruction = 8 rows x 128 bytes; lane p fills slot
     // p % 8 of row p / 8 and so fetches logical chunk (p % 8) ^ ((row / 2) % 8).
-    // Rows past the tile's re-read a valid row (their results are never stored).
+    // Rows past the descriptor's read 0 (their results are never stored).
     const uint8_t* base_a = a.CA;
     const uint8_t* base_b;
     uint32_t bytes_a, bytes_b;
@@ -141,30 +141,33 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
         bytes_b = (uint32_t)min(BN, a.N - n0) * (uint32_t)K;
     }
     const v4i rsrc_a = buffer_rsrc(base_a, bytes_a), rsrc_b = buffer_rsrc(base_b, bytes_b);
-    uint32_t voff_a[S::kDmaA], voff_b[S::kDmaB];
-    const int ch = ((lane & 7) ^ ((lane >> 4) & 3)) * 16;  // for even 8-row groups; odd ones flip bit 2
-    // byte of the row where this lane's chunk starts, for the 8-row group `grp`
-    auto chunk = [&](int grp) { return (grp & 1) ? ch ^ 64 : ch; };
+    // byte of the row where this lane's chunk starts, in even groups of 8 rows;
+    // odd groups flip bit 6
+    const uint32_t ch = ((lane & 7) ^ (lane >> 4)) * 16;
+    // rows of a wave's loads: A rows 8 kDmaA wave + 8 d + lane / 8 of the tile
+    // (kGateUp: of the tokens the tile's rows come from), B rows likewise; in
+    // kGateUp a consumer wave's 64 rows are the gates of its 32 channels, then
+    // the ups (channels past N read some other row: their h is set to 0)
+    uint32_t row_a[MODE == kGateUp ? S::kDmaA : 1];
+    if constexpr (MODE == kGateUp) {
 #pragma unroll
-    for (int i = 0; i < S::kDmaA; ++i) {
-        const int grp = S::kDmaA * wave + i, r = min(8 * grp + (lane >> 3), rows - 1);
-        uint32_t row = (uint32_t)r;
-        if constexpr (MODE == kGateUp) row = (uint32_t)a.row_token[row0 + r];
-        voff_a[i] = row * (uint32_t)K + chunk(grp);
-    }
-#pragma unroll
-    for (int i = 0; i < S::kDmaB; ++i) {
-        const int grp = S::kDmaB * wave + i, r = 8 * grp + (lane >> 3);
-        uint32_t row;
-        if constexpr (MODE == kGateUp) {
-            // a wave's 64 rows: gate of its 32 channels, then up of the same
-            const int c = min(n0 + (r >> 6) * 32 + (r & 31), a.N - 1);
-            row = (uint32_t)(c + ((r >> 5) & 1) * a.N);
-        } else {
-            row = (uint32_t)min(r, a.N - n0 - 1);
+        for (int d = 0; d < S::kDmaA; ++d) {
+            const int r = min(8 * (S::kDmaA * wave + d) + (lane >> 3), rows - 1);
+            row_a[d] = (uint32_t)a.row_token[row0 + r] * (uint32_t)K;
         }
-        voff_b[i] = row * (uint32_t)K + chunk(grp);
+    } else {
+        row_a[0] = (uint32_t)(8 * S::kDmaA * wave + (lane >> 3)) * (uint32_t)K;
     }
+    uint32_t row_b = (uint32_t)(lane >> 3);
+    if constexpr (MODE == kGateUp) {
+        const int r = 8 * S::kDmaB * wave;  // (a multiple of 32: whole halves)
+        static_assert(MODE != kGateUp || 8 * S::kDmaB % 32 == 0, "loads of a wave stay in one half");
+        row_b += (uint32_t)(n0 + (r >> 6) * 32);
+        row_b += (uint32_t)(((r >> 5) & 1) * a.N);
+    } else {
+        row_b += (uint32_t)(8 * S::kDmaB * wave);
+    }
+    row_b *= (uint32_t)K;
     // the row scales: lane p of each instruction one row of 64
     const float* sa_ptr;
     {
@@ -174,33 +177,56 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
         else
             sa_ptr = a.SCA + row0 + r;
     }
-    const uint32_t lds_ring = lds_address(ring);
-    const uint32_t lds_sa = lds_address(reinterpret_cast<const int8_t*>(s_sa)) + (64 * wave % S::kSa) * 4;
+    const uint32_t lds_ring = __builtin_amdgcn_readfirstlane(lds_address(ring));
+    const uint32_t lds_sa = __builtin_amdgcn_readfirstlane(lds_address(reinterpret_cast<const int8_t*>(s_sa)));
     const int half_kt = K % kStageK != 0 ? nkb - 1 : -1;  // the stage whose second half is past K
-    auto dma = [&](int kt, int u) {
+    // load d of a wave's kDma per stage: A rows, B rows, the row scales.  Past
+    // the last stage it re-reads that one, into a buffer nobody reads again.
+    constexpr int kDma = S::kDmaA + S::kDmaB + 1;
+    static_assert(S::kDmaB % 2 == 0 && (S::kDmaA % 2 == 0 || S::kDmaA == 1), "parity of the 8-row groups");
+    auto dma = [&](int d, int kt_want, int u) {
+        const int kt = min(kt_want, nkb - 1);
         const uint32_t kd = (uint32_t)kt * kStageK;
-#pragma unroll
-        for (int i = 0; i < S::kDmaA; ++i) {
-            const int grp = S::kDmaA * wave + i;
-            const uint32_t off = kt == half_kt && chunk(grp) >= 64 ? kPastEnd : voff_a[i] + kd;
-            dma_line(rsrc_a, off, lds_ring + u * S::kStageBytes + grp * 8 * kStageK);
+        if (d < S::kDmaA) {
+            const int grp = S::kDmaA * wave + d;
+            const uint32_t c = (S::kDmaA == 1 ? wave & 1 : d & 1) ? ch ^ 64 : ch;
+            const uint32_t row = MODE == kGateUp ? row_a[MODE == kGateUp ? d : 0] + kd
+                                                 : row_a[0] + (kd + (uint32_t)(8 * d) * (uint32_t)K);
+            dma_line(rsrc_a, kt == half_kt && c >= 64 ? kPastEnd : row + c,
+                     lds_ring + u * S::kStageBytes + grp * 8 * kStageK);
+        } else if (d < S::kDmaA + S::kDmaB) {
+            const int i = d - S::kDmaA, grp = S::kDmaB * wave + i;
+            const uint32_t c = (i & 1) ? ch ^ 64 : ch;
+            uint32_t step = (uint32_t)(8 * i);
+            if (MODE == kGateUp && i >= 4) step += (uint32_t)(a.N - 32);  // (a wave of 64 rows: its up half)
+            dma_line(rsrc_b, kt == half_kt && c >= 64 ? kPastEnd : row_b + (kd + step * (uint32_t)K) + c,
+                     lds_ring + u * S::kStageBytes + (BM + grp * 8) * kStageK);
+        } else {
+            dma4(sa_ptr + (int64_t)kt * a.ld_sa, lds_sa + (u * S::kSa + 64 * wave % S::kSa) * 4);
         }
-#pragma unroll
-        for (int i = 0; i < S::kDmaB; ++i) {
-            const int grp = S::kDmaB * wave + i;
-            const uint32_t off = kt == half_kt && chunk(grp) >= 64 ? kPastEnd : voff_b[i] + kd;
-            dma_line(rsrc_b, off, lds_ring + u * S::kStageBytes + (BM + grp * 8) * kStageK);
-        }
-        dma4(sa_ptr + (int64_t)kt * a.ld_sa, lds_sa + u * S::kSa * 4);
     };
 
     // ---- fragments: lane l holds 32 bytes of row (l % 16), chunks l / 16 and
-    // l / 16 + 4 (the same K order for both operands)
+    // l / 16 + 4 (the same K order for both operands).  The addresses of the
+    // wave's first rows in the current buffer; `other` leads to the other one.
+    constexpr int kWaveM = MT * 16, kWaveN = NT * 16;
     const int fr = lane & 15;
-    const uint32_t f_lo = fr * kStageK + (((lane >> 4) ^ (fr >> 1)) & 7) * 16, f_hi = f_lo ^ 64;
-    auto frag = [&](int u, int row) -> v8i {
-        const uint32_t at = u * S::kStageBytes + row * kStageK;
-        const v4i lo = lds_load<v4i>(ring, at + f_lo), hi = lds_load<v4i>(ring, at + f_hi);
+    const uint32_t f_lo = fr * kStageK + (((lane >> 4) ^ (fr >> 1)) & 7) * 16;
+    uint32_t at_x[2] = {lds_ring + wm * kWaveM * kStageK + f_lo, lds_ring + wm * kWaveM * kStageK + (f_lo ^ 64)};
+    uint32_t at_w[2] = {at_x[0] + (BM + wn * kWaveN - wm * kWaveM) * kStageK,
+                        at_x[1] + (BM + wn * kWaveN - wm * kWaveM) * kStageK};
+    uint32_t at_sa = lds_sa + (wm * kWaveM + fr) * 4;
+    int other = 1;
+    auto flip = [&]() {
+        at_x[0] += other * S::kStageBytes;
+        at_x[1] += other * S::kStageBytes;
+        at_w[0] += other * S::kStageBytes;
+        at_w[1] += other * S::kStageBytes;
+        at_sa += other * S::kSa * 4;
+        other = -other;
+    };
+    auto frag = [&](const uint32_t (&at)[2], int row) -> v8i {
+        const v4i lo = lds_at<v4i>(at[0] + row * kStageK), hi = lds_at<v4i>(at[1] + row * kStageK);
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
 
@@ -209,41 +235,85 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kWaveM = MT * 16, kWaveN = NT * 16;
     // which half's weight scale a wave's channel tiles take
-    const int half_of_wave = MODE == kGateUp ? 0 : wn * kWaveN / kBlock;
+    const float* sb_at = s_sb + (MODE == kGateUp ? 0 : wn * kWaveN / kBlock) * kMaxKb;
 
-    auto stage = [&](int kt, int u) {
-        wait_vmcnt<0>();
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS reads and writes are done
-        stage_barrier();
-        if (kt + 1 < nkb) dma(kt + 1, 1 - u);
-        const float sb0 = s_sb[half_of_wave * kMaxKb + kt];
-        const float sb1 = MODE == kGateUp ? s_sb[kMaxKb + kt] : sb0;
-        v8i w[NT];
+    // The K loop.  Row tile j's MFMAs fill p[j % 2] while the results of the
+    // row tile before are scaled and added; its activations are read one row
+    // tile ahead.  Between the stage's last two row tiles every wave waits for
+    // its loads of the next stage and its reads of this one, and meets the
+    // others: the next stage is in the other buffer, this one is free.  The last
+    // row tile reads the next stage's weights in place, and the loads of the
+    // stage after go out with it and with the first row tile that follows.
+    static_assert(MT % 2 == 0, "the row tiles alternate between two register sets");
+    v8i w[NT], x[2];
+    v4f p[2][NT];
+    float sa[2], sb0, sb1;
+    float f0 = 0.0f, f1 = 0.0f;  // scales of the results in flight (gate or all, up)
+    auto read_sa = [&](int j) { return lds_at<float>(at_sa + 64 * j); };
+    auto read_sb = [&](int kt) {
+        sb0 = sb_at[kt];
+        sb1 = MODE == kGateUp ? sb_at[kMaxKb + kt] : sb0;
+    };
+    auto add = [&](int i, int j, int set) {
+        const float f = MODE == kGateUp && i >= NT / 2 ? f1 : f0;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) w[i] = frag(u, BM + wn * kWaveN + 16 * i);
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[set][i][v], f, acc[i][j][v]);
+    };
+#pragma unroll
+    for (int i = 0; i < NT; ++i) p[1][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    auto stage = [&](int kt) {
+        const int u = kt & 1;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            const v8i x = frag(u, wm * kWaveM + 16 * j);
-            const float sa = s_sa[u * S::kSa + wm * kWaveM + 16 * j + fr];
-            const float f0 = sa * sb0, f1 = MODE == kGateUp ? sa * sb1 : f0;
+            if (j == MT - 1) {
+                __builtin_amdgcn_s_waitcnt(0);
+                stage_barrier();
+                flip();
+                x[0] = frag(at_x, 0);  // (x[0]'s last use has been issued)
+                sa[0] = read_sa(0);
+            } else {
+                x[(j + 1) & 1] = frag(at_x, 16 * (j + 1));
+                sa[(j + 1) & 1] = read_sa(j + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const v4f p = mfma_block(w[i], x);
-                const float f = MODE == kGateUp && i >= NT / 2 ? f1 : f0;
+                p[j & 1][i] = mfma_block(w[i], x[j & 1]);
+                if (j == MT - 1) w[i] = frag(at_w, 16 * i);
+                add(i, (j + MT - 1) % MT, (j + 1) & 1);
+                if (j == MT - 1)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], f, acc[i][j][v]);
+                    for (int d = i * (kDma / 2) / NT; d < (i + 1) * (kDma / 2) / NT; ++d) dma(d, kt + 2, u);
+                if (j == 0)
+#pragma unroll
+                    for (int d = kDma / 2 + i * (kDma - kDma / 2) / NT;
+                         d < kDma / 2 + (i + 1) * (kDma - kDma / 2) / NT; ++d)
+                        dma(d, kt + 1, 1 - u);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            f0 = sa[j & 1] * sb0;
+            f1 = MODE == kGateUp ? sa[j & 1] * sb1 : f0;
+            if (j == MT - 1) read_sb(min(kt + 1, nkb - 1));
         }
     };
-    dma(0, 0);
-    int kt = 0;
-    for (; kt + 2 <= nkb; kt += 2) {
-        stage(kt, 0);
-        stage(kt + 1, 1);
-    }
-    if (kt < nkb) stage(kt, 0);
+    // stage 0 whole, and the part of stage 1 that the last row tile of a stage
+    // before it would have loaded
+#pragma unroll
+    for (int d = 0; d < kDma; ++d) dma(d, 0, 0);
+    __builtin_amdgcn_s_waitcnt(0);
+    stage_barrier();
+#pragma unroll
+    for (int d = 0; d < kDma / 2; ++d) dma(d, 1, 1);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) w[i] = frag(at_w, 16 * i);
+    x[0] = frag(at_x, 0);
+    sa[0] = read_sa(0);
+    read_sb(0);
+    for (int kt = 0; kt < nkb; ++kt) stage(kt);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) add(i, MT - 1, (MT - 1) & 1);
+    wait_vmcnt<0>();  // the loads past the last stage have landed too
 
     // ---- results: lane l holds channels 4 (l / 16) .. + 3 of each 16-channel
     // tile for token row l % 16 of each 16-row tile
@@ -291,7 +361,7 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
         // channels from the four waves that share its rows
         static_assert(MODE != kGateUp || (NT == 4 && S::WN == 4), "gate and up of 32 channels per wave");
         float* red = reinterpret_cast<float*>(ring);  // [WN][BM]
-        stage_barrier();  // every wave is done with the ring (its own reads have returned)
+        __syncthreads();  // every wave's loads and reads of the ring are done
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             float m = 0.0f;
