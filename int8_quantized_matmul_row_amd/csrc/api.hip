@@ -570,6 +570,7 @@ llmint8_status llmint8_matmul_fp8_block(int dtype, int64_t M, int64_t N, int64_t
 
 size_t llmint8_linear_fp8_block_workspace_size(int64_t M, int64_t N, int64_t K) {
     if (check_block_sizes(M, N, K) != LLMINT8_OK || M == 0 || N == 0) return 0;
+    if (llmint8::linear_block_fused(M, N, K)) return 0;
     return block_act_layout(M, K).end + llmint8::gemm_block_workspace(M, N, K);
 }
 
@@ -586,6 +587,10 @@ llmint8_status llmint8_linear_fp8_block(const void* X, int dtype, int64_t M, int
         return LLMINT8_ERR_INVALID_ARGUMENT;
     if ((s = check_device()) != LLMINT8_OK) return s;
     llmint8::BlockGemmArgs a = block_gemm_args(dtype, M, N, K, CB, SCB, bias, Y);
+    if (llmint8::linear_block_fused(M, N, K)) {
+        hipError_t e = llmint8::launch_linear_block_fused(a, X, stream);
+        return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
+    }
     const BlockActLayout L = block_act_layout(M, K);
     char* ws = static_cast<char*>(workspace);
     uint8_t* ca = reinterpret_cast<uint8_t*>(ws);

@@ -355,6 +355,15 @@ __device__ __forceinline__ float wave_max(float v) {
     return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
 
+// max over the 16 lanes of a row of lanes, returned to all 16
+__device__ __forceinline__ float row16_max(float v) {
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0xB1>(0, __builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x4E>(0, __builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x141>(0, __builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x140>(0, __builtin_bit_cast(int, v))));
+    return v;
+}
+
 // inclusive prefix sum over the 64 lanes
 __device__ __forceinline__ int wave_incl_scan(int v) {
     v += dpp_i<0x111>(0, v);        // row_shr:1 (lanes without a source add 0)
@@ -379,6 +388,12 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 
 __device__ __forceinline__ int wave_sum(int v) {
     return __builtin_amdgcn_readlane(wave_incl_scan(v), 63);
+}
+
+// this wave's LDS accesses before it come before those after it
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // ---- LDS-DMA and explicit waits -------------------------------------------
@@ -611,6 +626,10 @@ struct BlockGemmArgs {
 };
 size_t gemm_block_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, hipStream_t stream);
+bool gemm_block_streams(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_block_stream(const BlockGemmArgs& a, hipStream_t stream);
+bool linear_block_fused(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear_block_fused(const BlockGemmArgs& a, const void* X, hipStream_t stream);
 int grouped_tile_rows(int64_t pairs, int E);
 hipError_t launch_experts_gate_up(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream);
 hipError_t launch_experts_down(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream);

@@ -444,9 +444,9 @@ hipError_t launch_dense(BlockGemmArgs a, hipStream_t stream) {
 
 hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, hipStream_t stream) {
     (void)workspace;
+    if (gemm_block_streams(a.M, a.N, a.K)) return launch_gemm_block_stream(a, stream);
     if (a.M > 512) return launch_dense<Tile256>(a, stream);
-    if (a.M > 64) return launch_dense<Tile128>(a, stream);
-    return launch_dense<Tile32>(a, stream);
+    return launch_dense<Tile128>(a, stream);
 }
 
 int grouped_tile_rows(int64_t pairs, int E) {

@@ -1,0 +1,319 @@
+// Block-scaled FP8 products of few rows, bound by the weight's bytes (or, with
+// a small grid of tiles, by latency): weights stream from memory straight into
+// the MFMA operand registers.
+//
+// A workgroup of 8 waves owns C x 16 channels (and G x 16 token rows) and the
+// whole of K: wave w takes the 128-blocks w, w + 8, ... of K, so that together
+// the waves read each weight row in order, and keeps the weights of kDepth
+// blocks in flight.  The waves' fp32 sums meet in LDS, are added in wave order
+// and leave as 16-bit Y.  For v_mfma_f32_16x16x128_f8f6f4 a lane holds 32 bytes
+// of a row: 16-byte chunks l / 16 and l / 16 + 4 of the block, the same for
+// both operands.
+#include "common.h"
+
+namespace llmint8 {
+
+namespace {
+
+constexpr int kWaves8 = 8;
+constexpr float kCodeScale = 1.0f / (448.0f * 448.0f);
+
+__device__ __forceinline__ v4f mfma_block(const v8i& w, const v8i& x) {
+    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// This lane's 32 bytes of block kb of the row `row_off` bytes into the buffer.
+// What lies past the buffer's rows, past K in a last half block, or in a block
+// the wave does not have (!in) reads 0 and moves no memory.
+constexpr uint32_t kPastEnd = 0xffffff00u;
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off, 0, 0));
+}
+__device__ __forceinline__ v8i load_codes(__amdgpu_buffer_rsrc_t rsrc, uint32_t row_off, int kb, bool in, int K,
+                                          int lane) {
+    const uint32_t off = row_off + (uint32_t)(kb * kBlock + (lane >> 4) * 16);
+    const v4i lo = load16(rsrc, in ? off : kPastEnd);
+    const v4i hi = load16(rsrc, in && kb * kBlock + 64 < K ? off + 64 : kPastEnd);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint8_t* base, int rows, int K) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)((uint32_t)rows * (uint32_t)K), 0x00020000);
+}
+
+// Codes of 8 values of one block, whose 16 lanes (q = 0..15) call it together;
+// returns the block's largest magnitude.
+__device__ __forceinline__ float block_codes(const float (&v)[8], uint2& codes) {
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(v[e]));
+    a = row16_max(a);
+    const float f = block_factor(a);
+    codes = make_uint2(e4m3_pack4(v[0], v[1], v[2], v[3], f), e4m3_pack4(v[4], v[5], v[6], v[7], f));
+    return a;
+}
+
+// A wave's quantized rows in LDS: block i, row r at (i * MR + r) * 128, chunk c
+// in slot c ^ ((r / 2) % 8).
+template <int MR>
+__device__ __forceinline__ uint32_t lds_row(int i, int r) {
+    return (uint32_t)(i * MR + r) * kBlock;
+}
+
+// ---- a dense product of up to 16 rows, X quantized on the way ----------------
+// Every workgroup quantizes the blocks of X that its own waves need (a wave
+// only its own blocks): M K values, read from L2, in place of a launch and a
+// round trip through memory.  X's loads go out before the weights'.
+template <int MR, int C, int kDepth, int kLds, bool BF16>
+__global__ __launch_bounds__(64 * kWaves8) void linear_stream_kernel(const uint16_t* __restrict__ X, int M, int N,
+                                                                     int K, const uint8_t* __restrict__ CB,
+                                                                     const float* __restrict__ SCB,
+                                                                     const uint16_t* __restrict__ bias,
+                                                                     uint16_t* __restrict__ Y) {
+    constexpr int kN = 16 * C, kRedRow = kN + 4;  // floats of a staged row (padding shifts banks)
+    constexpr int kRed = kWaves8 * MR * kRedRow * 4;
+    __shared__ __align__(16) int8_t smem[kLds > kRed ? kLds : kRed];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n0 = blockIdx.x * kN;
+    const int nkb = (K + kBlock - 1) / kBlock;
+    const int mine = (nkb - wave + kWaves8 - 1) / kWaves8;          // blocks of this wave
+    const int most = (nkb + kWaves8 - 1) / kWaves8;                 // of any wave
+    // each wave's codes, then each wave's scales [block][row]
+    int8_t* codes = smem + wave * most * MR * kBlock;
+    float* scales = reinterpret_cast<float*>(smem + kWaves8 * most * MR * kBlock) + wave * most * MR;
+
+    const __amdgpu_buffer_rsrc_t rsrc = rows_rsrc(CB + (size_t)n0 * K, min(kN, N - n0), K);
+    const uint32_t row = (uint32_t)(lane & 15) * (uint32_t)K;
+    const float* sb_at = SCB + (size_t)(n0 / kBlock) * nkb;  // (the channels of a workgroup share a block)
+    v8i w[kDepth][C];
+    float sb[kDepth];
+    auto fetch = [&](int d, int i) {
+        const int kb = kWaves8 * i + wave;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            w[d][c] = load_codes(rsrc, row + (uint32_t)(16 * c) * (uint32_t)K, kb, i < mine, K, lane);
+        sb[d] = sb_at[min(kb, nkb - 1)];
+    };
+    // ---- X: 16 lanes per (block, row), four of them per instruction
+    const int grp = lane >> 4, q = lane & 15;
+    const int units = mine * MR;
+    auto load_x = [&](int u) -> v8u16 {
+        const int i = u / MR, r = u % MR, k = (kWaves8 * i + wave) * kBlock + 8 * q;
+        return u < units && r < M && k < K ? *reinterpret_cast<const v8u16*>(X + (size_t)r * K + k)
+                                           : v8u16{0, 0, 0, 0, 0, 0, 0, 0};
+    };
+    auto put_x = [&](int u, const v8u16& x) {
+        if (u >= units) return;  // (all 16 lanes of a unit alike)
+        const int i = u / MR, r = u % MR;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = widen16<BF16>(x[e]);
+        uint2 c;
+        const float a = block_codes(v, c);
+        const int slot = (q >> 1) ^ ((r >> 1) & 7);
+        *reinterpret_cast<uint2*>(codes + lds_row<MR>(i, r) + slot * 16 + (q & 1) * 8) = c;
+        if (q == 0) scales[i * MR + r] = a;
+    };
+    constexpr int kAhead = 4;  // X loads in flight
+    v8u16 x[kAhead];
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) x[b] = load_x(4 * b + grp);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) fetch(d, d);
+    for (int u = 0; u < units; u += 4 * kAhead) {
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b) put_x(u + 4 * b + grp, x[b]);
+        if (u + 4 * kAhead < units)
+#pragma unroll
+            for (int b = 0; b < kAhead; ++b) x[b] = load_x(u + 4 * (kAhead + b) + grp);
+    }
+    wave_fence();
+    // ---- the products: block i's 16 x 16 results, scaled and added in fp32
+    v4f acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int m = min(lane & 15, MR - 1);  // (rows past M hold some row's values; never stored)
+    for (int i0 = 0; i0 < mine; i0 += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const int i = min(i0 + d, mine - 1);  // (past the wave's blocks: zero weights)
+            const int8_t* at = codes + lds_row<MR>(i, m);
+            const int slot = (lane >> 4) ^ ((m >> 1) & 7);
+            const v4i lo = *reinterpret_cast<const v4i*>(at + slot * 16);
+            const v4i hi = *reinterpret_cast<const v4i*>(at + (slot ^ 4) * 16);
+            const v8i xf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            const float f = scales[i * MR + m] * (sb[d] * kCodeScale);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const v4f p = mfma_block(w[d][c], xf);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[c][v] = __builtin_fmaf(p[v], f, acc[c][v]);
+            }
+            fetch(d, i0 + d + kDepth);
+        }
+    }
+    // ---- the waves' sums, in wave order
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem);  // [wave][row][channel]
+    if ((lane & 15) < MR)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            *reinterpret_cast<v4f*>(red + (wave * MR + (lane & 15)) * kRedRow + 16 * c + 4 * (lane >> 4)) = acc[c];
+    __syncthreads();
+    for (int o = tid; o < MR * kN; o += 64 * kWaves8) {
+        const int r = o / kN, n = o % kN;
+        if (r >= M || n0 + n >= N) continue;
+        float y = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWaves8; ++v) y += red[(v * MR + r) * kRedRow + n];
+        if (bias != nullptr) y += widen16<BF16>(bias[n0 + n]);
+        Y[(size_t)r * N + n0 + n] = narrow16<BF16>(y);
+    }
+}
+
+// ---- a dense product from codes, up to 16 G rows per workgroup ----------------
+template <int G, int C, int kDepth, bool BF16>
+__global__ __launch_bounds__(64 * kWaves8) void gemm_block_stream_kernel(BlockGemmArgs a) {
+    constexpr int kN = 16 * C, kRedRow = kN + 4;
+    __shared__ __align__(16) float red[kWaves8 * 16 * kRedRow];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = a.K, N = a.N, nkb = (K + kBlock - 1) / kBlock;
+    const int tiles_n = (N + kN - 1) / kN;
+    const int n0 = (int)(blockIdx.x % tiles_n) * kN;
+    const int m0 = (int)(blockIdx.x / tiles_n) * 16 * G;
+    const int rows = min(16 * G, a.M - m0);
+    const int mine = (nkb - wave + kWaves8 - 1) / kWaves8;
+    const __amdgpu_buffer_rsrc_t rsrc_w = rows_rsrc(a.CB + (size_t)n0 * K, min(kN, N - n0), K);
+    const __amdgpu_buffer_rsrc_t rsrc_x = rows_rsrc(a.CA + (size_t)m0 * K, rows, K);
+    const uint32_t row = (uint32_t)(lane & 15) * (uint32_t)K;
+    const float* sb_at = a.SCB + (size_t)(n0 / kBlock) * nkb;  // (the channels of a workgroup share a block)
+    const float* sa_at[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) sa_at[g] = a.SCA + m0 + min(16 * g + (lane & 15), rows - 1);
+    v8i w[kDepth][C], x[kDepth][G];
+    float sa[kDepth][G], sb[kDepth];
+    auto fetch = [&](int d, int i) {
+        const int kb = kWaves8 * i + wave, kc = min(kb, nkb - 1);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            w[d][c] = load_codes(rsrc_w, row + (uint32_t)(16 * c) * (uint32_t)K, kb, i < mine, K, lane);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            x[d][g] = load_codes(rsrc_x, row + (uint32_t)(16 * g) * (uint32_t)K, kb, i < mine, K, lane);
+            sa[d][g] = sa_at[g][(int64_t)kc * a.ld_sa];
+        }
+        sb[d] = sb_at[kc];
+    };
+    v4f acc[C][G];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[c][g] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) fetch(d, d);
+    for (int i0 = 0; i0 < mine; i0 += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float f = sa[d][g] * (sb[d] * kCodeScale);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const v4f p = mfma_block(w[d][c], x[d][g]);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[c][g][v] = __builtin_fmaf(p[v], f, acc[c][g][v]);
+                }
+            }
+            fetch(d, i0 + d + kDepth);
+        }
+    }
+    // the waves' sums of 16 rows at a time, in wave order
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        if (g > 0) __syncthreads();
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            *reinterpret_cast<v4f*>(red + (wave * 16 + (lane & 15)) * kRedRow + 16 * c + 4 * (lane >> 4)) = acc[c][g];
+        __syncthreads();
+        for (int o = tid; o < 16 * kN; o += 64 * kWaves8) {
+            const int r = o / kN, n = o % kN;
+            if (16 * g + r >= rows || n0 + n >= N) continue;
+            float y = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWaves8; ++v) y += red[(v * 16 + r) * kRedRow + n];
+            if (a.bias != nullptr) y += widen16<BF16>(a.bias[n0 + n]);
+            a.Y[(size_t)(m0 + 16 * g + r) * N + n0 + n] = narrow16<BF16>(y);
+        }
+    }
+}
+
+constexpr int64_t kMaxStreamN = (int64_t)1 << 27;  // the grid's threads stay below 2^32
+constexpr int kFusedLds = 66 * 1024;  // two workgroups per CU
+
+template <int MR, int C, int kDepth>
+void launch_fused(const BlockGemmArgs& a, const uint16_t* X, hipStream_t stream) {
+    const unsigned grid = (unsigned)((a.N + 16 * C - 1) / (16 * C));
+    if (a.bf16)
+        linear_stream_kernel<MR, C, kDepth, kFusedLds, true>
+            <<<grid, 64 * kWaves8, 0, stream>>>(X, a.M, a.N, a.K, a.CB, a.SCB, a.bias, a.Y);
+    else
+        linear_stream_kernel<MR, C, kDepth, kFusedLds, false>
+            <<<grid, 64 * kWaves8, 0, stream>>>(X, a.M, a.N, a.K, a.CB, a.SCB, a.bias, a.Y);
+}
+
+template <int G, int C, int kDepth>
+void launch_codes(const BlockGemmArgs& a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(((a.N + 16 * C - 1) / (16 * C)) * (((int64_t)a.M + 16 * G - 1) / (16 * G)));
+    if (a.bf16)
+        gemm_block_stream_kernel<G, C, kDepth, true><<<grid, 64 * kWaves8, 0, stream>>>(a);
+    else
+        gemm_block_stream_kernel<G, C, kDepth, false><<<grid, 64 * kWaves8, 0, stream>>>(a);
+}
+
+int row_class(int64_t M) { return M <= 1 ? 1 : M <= 4 ? 4 : M <= 8 ? 8 : 16; }
+
+}  // namespace
+
+// Whether the linear layer of M rows quantizes X inside the product: X's codes
+// of all of K fit the workgroup's LDS.
+bool linear_block_fused(int64_t M, int64_t N, int64_t K) {
+    if (M > 16 || N > kMaxStreamN) return false;
+    const int64_t per_wave = (K + kBlock * kWaves8 - 1) / (kBlock * kWaves8);
+    return per_wave * kWaves8 * row_class(M) * (kBlock + 4) <= kFusedLds;
+}
+
+hipError_t launch_linear_block_fused(const BlockGemmArgs& a, const void* X, hipStream_t stream) {
+    const uint16_t* x = static_cast<const uint16_t*>(X);
+    const bool wide = a.N >= 64 * 256;
+    switch (row_class(a.M)) {
+        case 1: wide ? launch_fused<1, 2, 4>(a, x, stream) : launch_fused<1, 1, 4>(a, x, stream); break;
+        case 4: wide ? launch_fused<4, 4, 2>(a, x, stream) : launch_fused<4, 1, 4>(a, x, stream); break;
+        case 8: wide ? launch_fused<8, 4, 2>(a, x, stream) : launch_fused<8, 1, 4>(a, x, stream); break;
+        default: wide ? launch_fused<16, 4, 2>(a, x, stream) : launch_fused<16, 1, 4>(a, x, stream); break;
+    }
+    return hipGetLastError();
+}
+
+// Whether the product of M rows streams its weights, past the fused one's rows.
+bool gemm_block_streams(int64_t M, int64_t N, int64_t K) {
+    (void)K;
+    if (N > kMaxStreamN) return false;
+    if (M <= 64) return true;
+    const int64_t tiles = ((M + 127) / 128) * ((N + 255) / 256);
+    return tiles < 64;
+}
+
+hipError_t launch_gemm_block_stream(const BlockGemmArgs& a, hipStream_t stream) {
+    const bool wide = a.N >= 64 * 256;
+    if (a.M <= 16)
+        wide ? launch_codes<1, 4, 2>(a, stream) : launch_codes<1, 1, 4>(a, stream);
+    else if (a.M <= 32)
+        wide ? launch_codes<2, 4, 2>(a, stream) : launch_codes<2, 1, 4>(a, stream);
+    else
+        wide ? launch_codes<4, 4, 1>(a, stream) : launch_codes<4, 2, 2>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace llmint8

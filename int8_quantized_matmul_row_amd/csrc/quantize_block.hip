@@ -11,15 +11,6 @@
 
 namespace llmint8 {
 
-// max over the 16 lanes of a row of lanes, returned to all 16
-__device__ __forceinline__ float row16_max(float v) {
-    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0xB1>(0, __builtin_bit_cast(int, v))));
-    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x4E>(0, __builtin_bit_cast(int, v))));
-    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x141>(0, __builtin_bit_cast(int, v))));
-    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x140>(0, __builtin_bit_cast(int, v))));
-    return v;
-}
-
 template <bool BF16>
 __device__ __forceinline__ float absmax8(const v8u16& v) {
     float a = 0.0f;

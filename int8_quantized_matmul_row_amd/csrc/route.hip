@@ -49,12 +49,6 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 
 constexpr int kRouteWaves = 4;
 
-// this wave's LDS accesses before it come before those after it
-__device__ __forceinline__ void wave_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // One token; keys: this wave's E words of LDS (used with groups only).
 template <int DT, int V>  // V: experts per lane, E <= 64 V
 __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, uint32_t* keys) {
