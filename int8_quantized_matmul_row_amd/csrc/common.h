@@ -495,6 +495,8 @@ __device__ __forceinline__ float block_factor(float a) {
     return a == 0.0f ? 0.0f : fminf(448.0f / a, 3.402823466e38f);
 }
 
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
 // ---- launchers (each returns hipGetLastError() after its launches) --------
 // fp8: E4M3 codes (scale 448/absmax) instead of int8 (127/absmax)
 hipError_t launch_quantize_weight(const void* W, bool bf16, bool fp8, int N, int K, int8_t* CB,
@@ -647,6 +649,8 @@ struct ExpertsArgs {
     const float* SCB2;
     uint16_t* Y;
 };
+bool experts_by_pair(int64_t pairs, int E, int K, int I);
+hipError_t launch_experts_by_pair(const ExpertsArgs& a, float* H, hipStream_t stream);  // H [T top_k, I]
 size_t experts_workspace(int64_t T, int E, int top_k, int K, int I);
 hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t stream);
 

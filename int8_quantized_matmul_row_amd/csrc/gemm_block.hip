@@ -371,7 +371,7 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const float g = acc[i][j][v], u = acc[i + NT / 2][j][v];
-                    const float h = in ? g / (1.0f + expf(-g)) * u : 0.0f;
+                    const float h = in ? silu(g) * u : 0.0f;
                     acc[i][j][v] = h;
                     m = fmaxf(m, fabsf(h));
                 }

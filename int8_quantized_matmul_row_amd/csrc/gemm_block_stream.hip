@@ -41,6 +41,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint8_t* base,
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)((uint32_t)rows * (uint32_t)K), 0x00020000);
 }
 
+// This lane's 32 bytes of a 128-byte row of codes in LDS, row r (chunk c in slot
+// c ^ ((r / 2) % 8)).
+__device__ __forceinline__ v8i read_codes(const int8_t* row, int r, int lane) {
+    const int slot = (lane >> 4) ^ ((r >> 1) & 7);
+    const v4i lo = *reinterpret_cast<const v4i*>(row + slot * 16);
+    const v4i hi = *reinterpret_cast<const v4i*>(row + (slot ^ 4) * 16);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 // Codes of 8 values of one block, whose 16 lanes (q = 0..15) call it together;
 // returns the block's largest magnitude.
 __device__ __forceinline__ float block_codes(const float (&v)[8], uint2& codes) {
@@ -60,40 +69,45 @@ __device__ __forceinline__ uint32_t lds_row(int i, int r) {
     return (uint32_t)(i * MR + r) * kBlock;
 }
 
-// ---- a dense product of up to 16 rows, X quantized on the way ----------------
-// Every workgroup quantizes the blocks of X that its own waves need (a wave
-// only its own blocks): M K values, read from L2, in place of a launch and a
-// round trip through memory.  X's loads go out before the weights'.
-template <int MR, int C, int kDepth, int kLds, bool BF16>
-__global__ __launch_bounds__(64 * kWaves8) void linear_stream_kernel(const uint16_t* __restrict__ X, int M, int N,
-                                                                     int K, const uint8_t* __restrict__ CB,
-                                                                     const float* __restrict__ SCB,
-                                                                     const uint16_t* __restrict__ bias,
-                                                                     uint16_t* __restrict__ Y) {
-    constexpr int kN = 16 * C, kRedRow = kN + 4;  // floats of a staged row (padding shifts banks)
-    constexpr int kRed = kWaves8 * MR * kRedRow * 4;
-    __shared__ __align__(16) int8_t smem[kLds > kRed ? kLds : kRed];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * kN;
+// ---- up to 16 rows, quantized on the way ---------------------------------------
+// The sums of one workgroup: C tiles of 16 weight rows against the 16-bit rows
+// X [M,K] (M <= MR), left in LDS as red[wave][row][tile channel] for the caller
+// to add up.  Every workgroup quantizes the blocks of X that its own waves need
+// (a wave only its own blocks): M K values, read from L2, in place of a launch
+// and a round trip through memory.  X's loads go out before the weights'.
+// Tile c: weight rows row0[c] .. + 15 of the buffer, block scales from sb_at[c].
+template <int MR, int C>
+struct StreamLds {
+    static constexpr int kRedRow = 16 * C + 4;  // floats of a staged row (padding shifts banks)
+    static constexpr int kRed = kWaves8 * MR * kRedRow * 4;
+};
+
+template <int MR, int C, int kDepth, bool BF16>
+__device__ __forceinline__ void stream_rows(int8_t* smem, const uint16_t* __restrict__ X, int M, int K,
+                                            __amdgpu_buffer_rsrc_t rsrc, const uint32_t (&row0)[C],
+                                            const float* const (&sb_at)[C]) {
+    constexpr int kRedRow = StreamLds<MR, C>::kRedRow;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nkb = (K + kBlock - 1) / kBlock;
-    const int mine = (nkb - wave + kWaves8 - 1) / kWaves8;          // blocks of this wave
-    const int most = (nkb + kWaves8 - 1) / kWaves8;                 // of any wave
+    const int mine = (nkb - wave + kWaves8 - 1) / kWaves8;  // blocks of this wave
+    const int most = (nkb + kWaves8 - 1) / kWaves8;         // of any wave
     // each wave's codes, then each wave's scales [block][row]
     int8_t* codes = smem + wave * most * MR * kBlock;
     float* scales = reinterpret_cast<float*>(smem + kWaves8 * most * MR * kBlock) + wave * most * MR;
 
-    const __amdgpu_buffer_rsrc_t rsrc = rows_rsrc(CB + (size_t)n0 * K, min(kN, N - n0), K);
-    const uint32_t row = (uint32_t)(lane & 15) * (uint32_t)K;
-    const float* sb_at = SCB + (size_t)(n0 / kBlock) * nkb;  // (the channels of a workgroup share a block)
     v8i w[kDepth][C];
-    float sb[kDepth];
+    float sb[kDepth][C];
     auto fetch = [&](int d, int i) {
         const int kb = kWaves8 * i + wave;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            w[d][c] = load_codes(rsrc, row + (uint32_t)(16 * c) * (uint32_t)K, kb, i < mine, K, lane);
-        sb[d] = sb_at[min(kb, nkb - 1)];
+        for (int c = 0; c < C; ++c) {
+            w[d][c] = load_codes(rsrc, (row0[c] + (uint32_t)(lane & 15)) * (uint32_t)K, kb, i < mine, K, lane);
+            if (c == 0 || sb_at[c] != sb_at[c - 1])
+                sb[d][c] = sb_at[c][min(kb, nkb - 1)];
+            else
+                sb[d][c] = sb[d][c - 1];
+        }
     };
     // ---- X: 16 lanes per (block, row), four of them per instruction
     const int grp = lane >> 4, q = lane & 15;
@@ -138,37 +152,175 @@ __global__ __launch_bounds__(64 * kWaves8) void linear_stream_kernel(const uint1
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {
             const int i = min(i0 + d, mine - 1);  // (past the wave's blocks: zero weights)
-            const int8_t* at = codes + lds_row<MR>(i, m);
-            const int slot = (lane >> 4) ^ ((m >> 1) & 7);
-            const v4i lo = *reinterpret_cast<const v4i*>(at + slot * 16);
-            const v4i hi = *reinterpret_cast<const v4i*>(at + (slot ^ 4) * 16);
-            const v8i xf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            const float f = scales[i * MR + m] * (sb[d] * kCodeScale);
+            const v8i xf = read_codes(codes + lds_row<MR>(i, m), m, lane);
+            const float sa = scales[i * MR + m] * kCodeScale;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const v4f p = mfma_block(w[d][c], xf);
+                const float f = sa * sb[d][c];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[c][v] = __builtin_fmaf(p[v], f, acc[c][v]);
             }
             fetch(d, i0 + d + kDepth);
         }
     }
-    // ---- the waves' sums, in wave order
     __syncthreads();
-    float* red = reinterpret_cast<float*>(smem);  // [wave][row][channel]
+    float* red = reinterpret_cast<float*>(smem);
     if ((lane & 15) < MR)
 #pragma unroll
         for (int c = 0; c < C; ++c)
             *reinterpret_cast<v4f*>(red + (wave * MR + (lane & 15)) * kRedRow + 16 * c + 4 * (lane >> 4)) = acc[c];
     __syncthreads();
-    for (int o = tid; o < MR * kN; o += 64 * kWaves8) {
+}
+
+// a row's channel, summed over the waves in their order
+template <int MR, int C>
+__device__ __forceinline__ float stream_sum(const int8_t* smem, int r, int n) {
+    const float* red = reinterpret_cast<const float*>(smem);
+    float y = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kWaves8; ++v) y += red[(v * MR + r) * StreamLds<MR, C>::kRedRow + n];
+    return y;
+}
+
+// The linear layer's forward for up to 16 rows.
+template <int MR, int C, int kDepth, int kLds, bool BF16>
+__global__ __launch_bounds__(64 * kWaves8) void linear_stream_kernel(const uint16_t* __restrict__ X, int M, int N,
+                                                                     int K, const uint8_t* __restrict__ CB,
+                                                                     const float* __restrict__ SCB,
+                                                                     const uint16_t* __restrict__ bias,
+                                                                     uint16_t* __restrict__ Y) {
+    constexpr int kN = 16 * C, kRed = StreamLds<MR, C>::kRed;
+    __shared__ __align__(16) int8_t smem[kLds > kRed ? kLds : kRed];
+    const int n0 = blockIdx.x * kN;
+    const int nkb = (K + kBlock - 1) / kBlock;
+    uint32_t row0[C];
+    const float* sb_at[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        row0[c] = 16 * c;
+        sb_at[c] = SCB + (size_t)(n0 / kBlock) * nkb;  // (the channels of a workgroup share a block)
+    }
+    stream_rows<MR, C, kDepth, BF16>(smem, X, M, K, rows_rsrc(CB + (size_t)n0 * K, min(kN, N - n0), K), row0, sb_at);
+    for (int o = threadIdx.x; o < MR * kN; o += 64 * kWaves8) {
         const int r = o / kN, n = o % kN;
         if (r >= M || n0 + n >= N) continue;
-        float y = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kWaves8; ++v) y += red[(v * MR + r) * kRedRow + n];
+        float y = stream_sum<MR, C>(smem, r, n);
         if (bias != nullptr) y += widen16<BF16>(bias[n0 + n]);
         Y[(size_t)r * N + n0 + n] = narrow16<BF16>(y);
+    }
+}
+
+// ---- single (token, slot) pairs of a mixture of experts --------------------------
+// With few pairs hardly two share an expert, and a workgroup takes one pair: its
+// expert comes straight from ids (no sort), h goes to memory in fp32.
+template <int CT, int kDepth, int kLds, bool BF16>
+__global__ __launch_bounds__(64 * kWaves8) void pair_gate_up_kernel(const uint16_t* __restrict__ X, int top_k, int K,
+                                                                    int I, int E, const int32_t* __restrict__ ids,
+                                                                    const uint8_t* __restrict__ CB13,
+                                                                    const float* __restrict__ SCB13,
+                                                                    float* __restrict__ H) {
+    constexpr int C = 2 * CT, kRed = StreamLds<1, C>::kRed;
+    __shared__ __align__(16) int8_t smem[kLds > kRed ? kLds : kRed];
+    const int tiles = I / (16 * CT);  // (I is a multiple of 64)
+    const int p = blockIdx.x / tiles, n0 = blockIdx.x % tiles * 16 * CT;
+    const int e = ids[p];
+    if ((uint32_t)e >= (uint32_t)E) return;
+    const int nkb = (K + kBlock - 1) / kBlock, nib = (I + kBlock - 1) / kBlock;
+    uint32_t row0[C];
+    const float* sb_at[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int up = c / CT;
+        row0[c] = (uint32_t)(up * I + n0 + 16 * (c % CT));
+        sb_at[c] = SCB13 + ((size_t)(2 * e + up) * nib + n0 / kBlock) * nkb;
+    }
+    const __amdgpu_buffer_rsrc_t rsrc = rows_rsrc(CB13 + (size_t)e * 2 * I * K, 2 * I, K);  // (below 2^32 bytes)
+    stream_rows<1, C, kDepth, BF16>(smem, X + (size_t)(p / top_k) * K, 1, K, rsrc, row0, sb_at);
+    const int n = threadIdx.x;
+    if (n < 16 * CT)
+        H[(size_t)p * I + n0 + n] =
+            silu(stream_sum<1, C>(smem, 0, n)) * stream_sum<1, C>(smem, 0, 16 * CT + n);
+}
+
+// Y of one token's 16 channels: wave w takes slots w, w + 8, ..., quantizes each
+// slot's h and multiplies it by its expert's 16 weight rows; the slots' results
+// are weighted and added in the order of the slots.
+template <int kDepth, int kLds, bool BF16>
+__global__ __launch_bounds__(64 * kWaves8) void pair_down_kernel(const float* __restrict__ H, int top_k, int K, int I,
+                                                                 int E, const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ weights,
+                                                                 const uint8_t* __restrict__ CB2,
+                                                                 const float* __restrict__ SCB2,
+                                                                 uint16_t* __restrict__ Y) {
+    __shared__ __align__(16) int8_t smem[kLds];
+    __shared__ float s_y[LLMINT8_TOP_K_MAX][16];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = K / 16;
+    const int64_t t = blockIdx.x / tiles;
+    const int n0 = blockIdx.x % tiles * 16;
+    const int nib = (I + kBlock - 1) / kBlock, nkb = (K + kBlock - 1) / kBlock;
+    int8_t* codes = smem + wave * nib * kBlock;
+    float* scales = reinterpret_cast<float*>(smem + kWaves8 * nib * kBlock) + wave * nib;
+    const int grp = lane >> 4, q = lane & 15;
+    for (int j = wave; j < top_k; j += kWaves8) {
+        const int e = __builtin_amdgcn_readfirstlane(ids[t * top_k + j]);
+        if ((uint32_t)e >= (uint32_t)E) continue;
+        const float* h = H + (size_t)(t * top_k + j) * I;
+        const __amdgpu_buffer_rsrc_t rsrc = rows_rsrc(CB2 + ((size_t)e * K + n0) * I, 16, I);
+        const float* sb_at = SCB2 + ((size_t)e * nkb + n0 / kBlock) * nib;
+        v8i w[kDepth];
+        float sb[kDepth];
+        auto fetch = [&](int d, int b) {
+            w[d] = load_codes(rsrc, (uint32_t)(lane & 15) * (uint32_t)I, b, b < nib, I, lane);
+            sb[d] = sb_at[min(b, nib - 1)];
+        };
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) fetch(d, d);
+        wave_fence();  // the last slot's codes have been read
+        for (int b = grp; b < nib; b += 4) {
+            const int k = b * kBlock + 8 * q;
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = 0.0f;
+            if (k < I) {
+                const v4f lo = *reinterpret_cast<const v4f*>(h + k), hi = *reinterpret_cast<const v4f*>(h + k + 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    v[x] = lo[x];
+                    v[4 + x] = hi[x];
+                }
+            }
+            uint2 c;
+            const float a = block_codes(v, c);
+            *reinterpret_cast<uint2*>(codes + b * kBlock + 8 * q) = c;
+            if (q == 0) scales[b] = a;
+        }
+        wave_fence();
+        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int b0 = 0; b0 < nib; b0 += kDepth) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                const int b = min(b0 + d, nib - 1);  // (past the last block: zero weights)
+                const v8i xf = read_codes(codes + b * kBlock, 0, lane);
+                const v4f p = mfma_block(w[d], xf);
+                const float f = scales[b] * kCodeScale * sb[d];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(p[v], f, acc[v]);
+                fetch(d, b0 + d + kDepth);
+            }
+        }
+        if ((lane & 15) == 0) *reinterpret_cast<v4f*>(&s_y[j][4 * (lane >> 4)]) = acc;
+    }
+    __syncthreads();
+    const int n = threadIdx.x;
+    if (n < 16) {
+        float y = 0.0f;
+        for (int j = 0; j < top_k; ++j)
+            if ((uint32_t)ids[t * top_k + j] < (uint32_t)E)
+                y = __builtin_fmaf(weights[t * top_k + j], s_y[j][n], y);
+        Y[t * K + n0 + n] = narrow16<BF16>(y);
     }
 }
 
@@ -249,6 +401,8 @@ __global__ __launch_bounds__(64 * kWaves8) void gemm_block_stream_kernel(BlockGe
     }
 }
 
+constexpr int kPairLds = 36 * 1024;  // four workgroups per CU
+constexpr int kMaxPairs = 64;  // tokens x slots that run pair by pair, at most
 constexpr int64_t kMaxStreamN = (int64_t)1 << 27;  // the grid's threads stay below 2^32
 constexpr int kFusedLds = 66 * 1024;  // two workgroups per CU
 
@@ -292,6 +446,35 @@ hipError_t launch_linear_block_fused(const BlockGemmArgs& a, const void* X, hipS
         case 4: wide ? launch_fused<4, 4, 2>(a, x, stream) : launch_fused<4, 1, 4>(a, x, stream); break;
         case 8: wide ? launch_fused<8, 4, 2>(a, x, stream) : launch_fused<8, 1, 4>(a, x, stream); break;
         default: wide ? launch_fused<16, 4, 2>(a, x, stream) : launch_fused<16, 1, 4>(a, x, stream); break;
+    }
+    return hipGetLastError();
+}
+
+// Whether the experts run pair by pair: few enough pairs that not many share an
+// expert (a shared one's weights are read again, from L2 at best), and a pair's
+// codes of X and of h fit the workgroup's LDS.  Top 8 of 64 experts, K = 4096,
+// I = 1024, against the sorted tiles: 5 tokens 92 against 115 us, 8 tokens 140
+// against 157.
+bool experts_by_pair(int64_t pairs, int E, int K, int I) {
+    if (pairs > kMaxPairs || pairs > E) return false;
+    const int64_t x_blocks = (K + kBlock * kWaves8 - 1) / (kBlock * kWaves8) * kWaves8;
+    const int64_t h_blocks = (int64_t)((I + kBlock - 1) / kBlock) * kWaves8;
+    return x_blocks * (kBlock + 4) <= kPairLds && h_blocks * (kBlock + 4) <= kPairLds;
+}
+
+hipError_t launch_experts_by_pair(const ExpertsArgs& a, float* H, hipStream_t stream) {
+    const int P = (int)a.T * a.top_k;
+    const unsigned up = (unsigned)(P * (a.I / 16)), down = (unsigned)(a.T * (a.K / 16));
+    if (a.bf16) {
+        pair_gate_up_kernel<1, 4, kPairLds, true><<<up, 64 * kWaves8, 0, stream>>>(a.X, a.top_k, a.K, a.I, a.E, a.ids,
+                                                                                   a.CB13, a.SCB13, H);
+        pair_down_kernel<8, kPairLds, true><<<down, 64 * kWaves8, 0, stream>>>(H, a.top_k, a.K, a.I, a.E, a.ids,
+                                                                               a.weights, a.CB2, a.SCB2, a.Y);
+    } else {
+        pair_gate_up_kernel<1, 4, kPairLds, false><<<up, 64 * kWaves8, 0, stream>>>(a.X, a.top_k, a.K, a.I, a.E,
+                                                                                    a.ids, a.CB13, a.SCB13, H);
+        pair_down_kernel<8, kPairLds, false><<<down, 64 * kWaves8, 0, stream>>>(H, a.top_k, a.K, a.I, a.E, a.ids,
+                                                                                a.weights, a.CB2, a.SCB2, a.Y);
     }
     return hipGetLastError();
 }

@@ -113,6 +113,26 @@ def test_rows_of_tokens_that_no_expert_takes_are_not_read():
     close(Y, want, "f16")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,k,K,I", [(1, 1, 64, 64), (2, 3, 192, 320), (3, 4, 1088, 64), (1, 12, 256, 1088),
+                                     (4, 3, 4160, 128)])
+def test_few_pairs_of_many_experts(T, k, K, I, dtype):
+    """Decode: fewer pairs than half the experts; some dropped, one expert twice."""
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    E = 2 * T * k
+    x, q13, q2, xv, w13, w2 = make(T, E, K, I, dtype, T + K)
+    g = torch.Generator().manual_seed(K)
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    if k > 2:
+        ids[T - 1, 0], ids[0, 1], ids[0, 2] = -1, E, int(ids[0, 0])
+    weights = torch.randn(T, k, generator=g)
+    Y = pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2)
+    close(Y, ref.experts(xv, ids.numpy(), weights.numpy(), w13, w2), dtype)
+    ids[:] = -1
+    assert (pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2) == 0).all()
+
+
 def test_no_tokens():
     import torch
     import int8_quantized_matmul_row_amd as pkg
