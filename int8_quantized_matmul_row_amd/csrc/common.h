@@ -495,7 +495,14 @@ __device__ __forceinline__ float block_factor(float a) {
     return a == 0.0f ? 0.0f : fminf(448.0f / a, 3.402823466e38f);
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// g / (1 + exp(-g)) to a few fp32 roundings: exp2 and reciprocal in one
+// instruction each (a tile of the gate/up product takes 32768 of them)
+__device__ __forceinline__ float silu(float g) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+}
+
+// the experts' down product leaves as integers of at most this magnitude
+constexpr float kPartMax = 32767.0f;
 
 // ---- launchers (each returns hipGetLastError() after its launches) --------
 // fp8: E4M3 codes (scale 448/absmax) instead of int8 (127/absmax)
@@ -608,7 +615,8 @@ hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t stream);
 // SCB [ceil(N/128), ceil(K/128)].  Dense: Y (+ bias).  Grouped by expert: the
 // tile list `tiles` (count, 3 words unused, then {expert, first row, rows, -}
 // each) and one [N,K] weight per expert, or [2,N,K] for gate and up, whose
-// rows are gathered by row_token and whose result goes to H / SH.
+// rows are gathered by row_token and whose result goes to H / SH; the down product's
+// goes to part / part_scale.
 struct BlockGemmArgs {
     bool bf16 = false;
     const uint8_t* CA = nullptr;
@@ -624,7 +632,10 @@ struct BlockGemmArgs {
     uint8_t* H = nullptr;
     float* SH = nullptr;
     int64_t ld_sh = 0;
-    float* part = nullptr;
+    uint16_t* part = nullptr;     // [rows, N] 16-bit integers, row r's block b
+    float* part_scale = nullptr;  // times part_scale[b * ld_part + r]
+    int64_t ld_part = 0;
+    int tile_rows = 0;  // dense tiles: set by the launcher
 };
 size_t gemm_block_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, hipStream_t stream);

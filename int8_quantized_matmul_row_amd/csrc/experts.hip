@@ -30,10 +30,11 @@ __device__ __forceinline__ int block_excl_scan(int v, int* waves, int* total) {
 
 // One workgroup: counts the pairs of each expert, lays the experts' rows out
 // one after another, gives every pair its row (in no particular order within
-// an expert: a row's results do not depend on its place) and lists the tiles
-// of `tile_rows` rows.  Pairs whose id is outside [0, E) get row -1.
+// an expert: a row's results do not depend on its place) and lists the tiles:
+// as few of at most `tile_rows` rows as hold an expert's, of even size in units
+// of `unit` rows.  Pairs whose id is outside [0, E) get row -1.
 __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
-                                                                  int top_k, int E, int tile_rows,
+                                                                  int top_k, int E, int tile_rows, int unit,
                                                                   int32_t* __restrict__ pair_row,
                                                                   int32_t* __restrict__ row_token,
                                                                   int32_t* __restrict__ tiles) {
@@ -53,11 +54,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
     const int nt = (c + tile_rows - 1) / tile_rows;
     const int t0 = block_excl_scan(nt, waves, &total);
     if (tid == 0) tiles[0] = total;
+    const int step = nt > 0 ? ((c + unit - 1) / unit + nt - 1) / nt * unit : 0;
     for (int t = 0; t < nt; ++t) {
         int32_t* out = tiles + 4 + 4 * (t0 + t);
         out[0] = tid;
-        out[1] = first + t * tile_rows;
-        out[2] = min(tile_rows, c - t * tile_rows);
+        out[1] = first + t * step;
+        out[2] = min(step, c - t * step);
     }
     __syncthreads();
     for (int p = tid; p < pairs; p += kSortThreads) {
@@ -71,36 +73,45 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
     }
 }
 
-// Y[t, :] = sum_j w[t, j] * part[row(t, j), :], in fp32 and in the order of j,
-// rounded once.  A thread holds 4 columns of one token.
+// Y[t, :] = sum_j w[t, j] * part[row(t, j), :] * part_scale, in fp32 and in the
+// order of j, rounded once.  A thread holds 8 columns of one token.
 template <bool BF16>
-__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ part,
+__global__ __launch_bounds__(256) void combine_kernel(const int16_t* __restrict__ part,
+                                                      const float* __restrict__ part_scale, int64_t ld_part,
                                                       const int32_t* __restrict__ pair_row,
                                                       const float* __restrict__ weights, int T, int K, int top_k,
                                                       uint16_t* __restrict__ Y) {
-    const int64_t quads = (int64_t)T * (K >> 2);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / (K >> 2);
-        const int c = (int)(i - t * (K >> 2)) * 4;
-        v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int per_row = K >> 3;
+    const int64_t items = (int64_t)T * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per_row;
+        const int c = (int)(i - t * per_row) * 8;
+        const float* scale = part_scale + (c / kBlock) * ld_part;
+        float y[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y[q] = 0.0f;
+#pragma unroll 4
         for (int j = 0; j < top_k; ++j) {
             const int row = pair_row[t * top_k + j];
             if (row < 0) continue;
-            const float w = weights[t * top_k + j];
-            const v4f v = *reinterpret_cast<const v4f*>(part + (size_t)row * K + c);
+            const float w = weights[t * top_k + j] * scale[row];
+            const v4i v = *reinterpret_cast<const v4i*>(part + (size_t)row * K + c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(w, v[q], y[q]);
+            for (int q = 0; q < 8; ++q)
+                y[q] = __builtin_fmaf(w, (float)(int16_t)((uint32_t)v[q >> 1] >> (16 * (q & 1))), y[q]);
         }
-        *reinterpret_cast<uint2*>(Y + t * K + c) =
-            make_uint2(narrow16<BF16>(y[0]) | (uint32_t)narrow16<BF16>(y[1]) << 16,
-                       narrow16<BF16>(y[2]) | (uint32_t)narrow16<BF16>(y[3]) << 16);
+        uint32_t out[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            out[q] = narrow16<BF16>(y[2 * q]) | (uint32_t)narrow16<BF16>(y[2 * q + 1]) << 16;
+        *reinterpret_cast<uint4*>(Y + t * K + c) = make_uint4(out[0], out[1], out[2], out[3]);
     }
 }
 
 // A chunk of tokens and its share of the workspace.
 struct ExpertsLayout {
     int64_t tokens;  // of a chunk
-    size_t ca, sca, pair_row, row_token, tiles, h, sh, part, total;
+    size_t ca, sca, pair_row, row_token, tiles, h, sh, part, part_scale, total;
 };
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -115,7 +126,7 @@ constexpr int64_t kChunkBytes = (int64_t)1 << 30;
 
 ExpertsLayout layout(int64_t T, int E, int top_k, int K, int I) {
     ExpertsLayout L;
-    int64_t most = kChunkBytes / ((int64_t)top_k * K * 4);
+    int64_t most = kChunkBytes / ((int64_t)top_k * K * 2);
     if (most > 0xf0000000ll / K) most = 0xf0000000ll / K;
     if (most < 1) most = 1;
     L.tokens = T < most ? T : most;
@@ -134,7 +145,8 @@ ExpertsLayout layout(int64_t T, int E, int top_k, int K, int I) {
     L.tiles = take(16 + 16 * (size_t)max_tiles(P, E, 32));
     L.h = take((size_t)P * I);
     L.sh = take((size_t)nib * P * 4);
-    L.part = take((size_t)P * K * 4);
+    L.part = take((size_t)P * K * 2);
+    L.part_scale = take((size_t)nkb * P * 4);
     L.total = at;
     return L;
 }
@@ -163,10 +175,12 @@ hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t str
         int32_t* tiles = reinterpret_cast<int32_t*>(ws + L.tiles);
         uint8_t* h = reinterpret_cast<uint8_t*>(ws + L.h);
         float* sh = reinterpret_cast<float*>(ws + L.sh);
-        float* part = reinterpret_cast<float*>(ws + L.part);
+        uint16_t* part = reinterpret_cast<uint16_t*>(ws + L.part);
+        float* part_scale = reinterpret_cast<float*>(ws + L.part_scale);
         hipError_t e = launch_quantize_act_block(a.X + (size_t)t0 * a.K, a.bf16, n, a.K, ca, sca, stream);
         if (e != hipSuccess) return e;
-        sort_pairs_kernel<<<1, kSortThreads, 0, stream>>>(a.ids + t0 * a.top_k, P, a.top_k, a.E, tile_rows, pair_row,
+        sort_pairs_kernel<<<1, kSortThreads, 0, stream>>>(a.ids + t0 * a.top_k, P, a.top_k, a.E, tile_rows,
+                                                          tile_rows < 64 ? tile_rows : 64, pair_row,
                                                           row_token, tiles);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         BlockGemmArgs g;
@@ -195,15 +209,19 @@ hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t str
         g.N = a.K;
         g.K = a.I;
         g.part = part;
+        g.part_scale = part_scale;
+        g.ld_part = P;
         if ((e = launch_experts_down(g, tile_rows, mt, stream)) != hipSuccess) return e;
-        const int64_t blocks = ((int64_t)n * (a.K / 4) + 255) / 256;
+        const int64_t blocks = ((int64_t)n * (a.K / 8) + 255) / 256;
         const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
         uint16_t* y = a.Y + (size_t)t0 * a.K;
         const float* w = a.weights + t0 * a.top_k;
         if (a.bf16)
-            combine_kernel<true><<<grid, 256, 0, stream>>>(part, pair_row, w, n, a.K, a.top_k, y);
+            combine_kernel<true><<<grid, 256, 0, stream>>>(reinterpret_cast<const int16_t*>(part), part_scale, P, pair_row,
+                                                           w, n, a.K, a.top_k, y);
         else
-            combine_kernel<false><<<grid, 256, 0, stream>>>(part, pair_row, w, n, a.K, a.top_k, y);
+            combine_kernel<false><<<grid, 256, 0, stream>>>(reinterpret_cast<const int16_t*>(part), part_scale, P, pair_row,
+                                                           w, n, a.K, a.top_k, y);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;

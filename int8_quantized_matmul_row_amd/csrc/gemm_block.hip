@@ -5,8 +5,11 @@
 //   kGateUp  rows gathered from the tokens' codes, weight rows n and I + n
 //            (gate and up) side by side in one tile; h = silu(g) * u leaves
 //            the tile as E4M3 codes with one scale per 128 channels;
-//   kDown    h's codes against the down weights, fp32 rows out (a later
-//            kernel weights and sums a token's rows).
+//   kDown    h's codes against the down weights; rows out as 16-bit integers with
+//            one scale per 128 channels (a later kernel weights and sums a
+//            token's rows).  fp32 rows would be twice the bytes, the largest
+//            share of the prefill's traffic; the integers are within 2^-16 of a
+//            block's largest value, below the rounding of a 16-bit Y.
 //
 // One v_mfma_f32_16x16x128_f8f6f4 covers a whole scale block of K, from a zero
 // accumulator; its 16 x 16 result is then added into fp32 registers times the
@@ -58,71 +61,33 @@ __device__ __forceinline__ int xcd_order(int b, int total) {
     return x * q + min(x, r) + (b >> 3);
 }
 
-template <int BM_, int WM_, int WN_>
+// A workgroup's waves stand WM x WN on its tile; every wave has NT = 4 channel
+// tiles of 16 and up to kMaxMT row tiles of 16.
+template <int WM_, int WN_, int kMaxMT_>
 struct Shape {
-    static constexpr int BM = BM_, BN = 256, WM = WM_, WN = WN_, NW = WM * WN;
-    static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;  // 16 x 16 tiles of a wave
+    static constexpr int WM = WM_, WN = WN_, NW = WM * WN, kMaxMT = kMaxMT_;
+    static constexpr int BM = 16 * WM * kMaxMT, BN = 256, NT = BN / WN / 16;
     static constexpr int kStageBytes = (BM + BN) * kStageK;
     static constexpr int kSa = BM < 64 ? 64 : BM;  // floats of a stage's row scales
-    static constexpr int kDmaA = BM / 8 / NW, kDmaB = BN / 8 / NW;
-    static_assert(kDmaA * 8 * NW == BM && kDmaB * 8 * NW == BN, "whole loads per wave");
-    static_assert(NT * 16 * WN == BN && MT * 16 * WM == BM, "whole tiles per wave");
+    static_assert(NT == 4 && WN == 4, "a wave's 64 channels: half a weight block, or gate and up of 32");
 };
 
-template <typename S, int MODE, bool BF16>
-__global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a) {
-    __shared__ __align__(1024) int8_t ring[2 * S::kStageBytes];
-    __shared__ float s_sa[2 * S::kSa];
-    __shared__ float s_sb[2 * kMaxKb];
-    constexpr int BM = S::BM, BN = S::BN, MT = S::MT, NT = S::NT;
+struct Tile {
+    int row0, rows, n0, e;  // rows [row0, row0 + rows), channels from n0 of weight matrix e
+};
+
+// The tile's work with MT row tiles per wave (rows <= 16 WM MT).
+template <typename S, int MODE, bool BF16, int MT>
+__device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& tile, int8_t* ring, float* s_sa,
+                                          float* s_sb) {
+    constexpr int BM = 16 * S::WM * MT, BN = S::BN, NT = S::NT;
+    constexpr int kDmaA = BM / 8 / S::NW, kDmaB = BN / 8 / S::NW;  // 8-row loads per wave and stage
+    static_assert(kDmaB * 8 * S::NW == BN && kDmaA * 8 * S::NW == BM, "whole loads per wave");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
     const int K = a.K, nkb = (K + kBlock - 1) / kBlock;
-    const int chans = MODE == kGateUp ? BN / 2 : BN;  // output channels of a tile
-    const int tiles_n = (a.N + chans - 1) / chans;
-
-    // ---- which tile: rows [row0, row0 + rows) of the (sorted) activations,
-    // channels from n0 of weight matrix `e`
-    int row0, rows, n0, e = 0;
-    if constexpr (MODE == kDense) {
-        constexpr int kGroupM = 4;  // tile rows that share a weight panel in L2
-        const int tiles_m = (int)(((int64_t)a.M + BM - 1) / BM);
-        const int L = xcd_order(blockIdx.x, tiles_m * tiles_n);
-        const int first = L / (kGroupM * tiles_n) * kGroupM;
-        const int gsz = min(tiles_m - first, kGroupM), in = L - first * tiles_n;
-        row0 = (first + in % gsz) * BM;
-        n0 = in / gsz * chans;
-        rows = min(BM, a.M - row0);
-    } else {
-        const int total = a.tiles[0] * tiles_n;
-        if ((int)blockIdx.x >= total) return;
-        const int L = xcd_order(blockIdx.x, total);
-        const int32_t* t = a.tiles + 4 + 4 * (L / tiles_n);
-        e = __builtin_amdgcn_readfirstlane(t[0]);
-        row0 = __builtin_amdgcn_readfirstlane(t[1]);
-        rows = __builtin_amdgcn_readfirstlane(t[2]);
-        n0 = L % tiles_n * chans;
-    }
-
-    // ---- weight block scales of the tile's two 128-channel halves (gate and
-    // up, or channels n0.. and n0 + 128..), with the codes' 1/448^2
-    const int nnb = (a.N + kBlock - 1) / kBlock;
-    {
-        const float* sb0;
-        const float* sb1;
-        if constexpr (MODE == kGateUp) {
-            sb0 = a.SCB + ((size_t)e * 2 * nnb + n0 / kBlock) * nkb;
-            sb1 = sb0 + (size_t)nnb * nkb;
-        } else {
-            sb0 = a.SCB + ((size_t)e * nnb + n0 / kBlock) * nkb;
-            sb1 = n0 + kBlock < a.N ? sb0 + nkb : sb0;
-        }
-        for (int i = tid; i < nkb; i += 64 * S::NW) {
-            s_sb[i] = sb0[i] * kCodeScale;
-            s_sb[kMaxKb + i] = sb1[i] * kCodeScale;
-        }
-    }
+    const int row0 = tile.row0, rows = tile.rows, n0 = tile.n0, e = tile.e;
 
     // ---- stage loads: one instruction = 8 rows x 128 bytes; lane p fills slot
     // p % 8 of row p / 8 and so fetches logical chunk (p % 8) ^ ((row / 2) % 8).
@@ -148,24 +113,24 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
     // (kGateUp: of the tokens the tile's rows come from), B rows likewise; in
     // kGateUp a consumer wave's 64 rows are the gates of its 32 channels, then
     // the ups (channels past N read some other row: their h is set to 0)
-    uint32_t row_a[MODE == kGateUp ? S::kDmaA : 1];
+    uint32_t row_a[MODE == kGateUp ? kDmaA : 1];
     if constexpr (MODE == kGateUp) {
 #pragma unroll
-        for (int d = 0; d < S::kDmaA; ++d) {
-            const int r = min(8 * (S::kDmaA * wave + d) + (lane >> 3), rows - 1);
+        for (int d = 0; d < kDmaA; ++d) {
+            const int r = min(8 * (kDmaA * wave + d) + (lane >> 3), rows - 1);
             row_a[d] = (uint32_t)a.row_token[row0 + r] * (uint32_t)K;
         }
     } else {
-        row_a[0] = (uint32_t)(8 * S::kDmaA * wave + (lane >> 3)) * (uint32_t)K;
+        row_a[0] = (uint32_t)(8 * kDmaA * wave + (lane >> 3)) * (uint32_t)K;
     }
     uint32_t row_b = (uint32_t)(lane >> 3);
     if constexpr (MODE == kGateUp) {
-        const int r = 8 * S::kDmaB * wave;  // (a multiple of 32: whole halves)
-        static_assert(MODE != kGateUp || 8 * S::kDmaB % 32 == 0, "loads of a wave stay in one half");
+        const int r = 8 * kDmaB * wave;  // (a multiple of 32: whole halves)
+        static_assert(MODE != kGateUp || 8 * kDmaB % 32 == 0, "loads of a wave stay in one half");
         row_b += (uint32_t)(n0 + (r >> 6) * 32);
         row_b += (uint32_t)(((r >> 5) & 1) * a.N);
     } else {
-        row_b += (uint32_t)(8 * S::kDmaB * wave);
+        row_b += (uint32_t)(8 * kDmaB * wave);
     }
     row_b *= (uint32_t)K;
     // the row scales: lane p of each instruction one row of 64
@@ -182,25 +147,25 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
     const int half_kt = K % kStageK != 0 ? nkb - 1 : -1;  // the stage whose second half is past K
     // load d of a wave's kDma per stage: A rows, B rows, the row scales.  Past
     // the last stage it re-reads that one, into a buffer nobody reads again.
-    constexpr int kDma = S::kDmaA + S::kDmaB + 1;
-    static_assert(S::kDmaB % 2 == 0 && (S::kDmaA % 2 == 0 || S::kDmaA == 1), "parity of the 8-row groups");
+    constexpr int kDma = kDmaA + kDmaB + 1;
+    static_assert(kDmaB % 2 == 0, "parity of the 8-row groups");
     auto dma = [&](int d, int kt_want, int u) {
         const int kt = min(kt_want, nkb - 1);
         const uint32_t kd = (uint32_t)kt * kStageK;
-        if (d < S::kDmaA) {
-            const int grp = S::kDmaA * wave + d;
-            const uint32_t c = (S::kDmaA == 1 ? wave & 1 : d & 1) ? ch ^ 64 : ch;
+        if (d < kDmaA) {
+            const int grp = kDmaA * wave + d;
+            const uint32_t c = ch ^ ((uint32_t)((kDmaA % 2 == 0 ? d : wave + d) & 1) << 6);
             const uint32_t row = MODE == kGateUp ? row_a[MODE == kGateUp ? d : 0] + kd
                                                  : row_a[0] + (kd + (uint32_t)(8 * d) * (uint32_t)K);
             dma_line(rsrc_a, kt == half_kt && c >= 64 ? kPastEnd : row + c,
                      lds_ring + u * S::kStageBytes + grp * 8 * kStageK);
-        } else if (d < S::kDmaA + S::kDmaB) {
-            const int i = d - S::kDmaA, grp = S::kDmaB * wave + i;
-            const uint32_t c = (i & 1) ? ch ^ 64 : ch;
+        } else if (d < kDmaA + kDmaB) {
+            const int i = d - kDmaA, grp = kDmaB * wave + i;
+            const uint32_t c = ch ^ ((uint32_t)(i & 1) << 6);
             uint32_t step = (uint32_t)(8 * i);
             if (MODE == kGateUp && i >= 4) step += (uint32_t)(a.N - 32);  // (a wave of 64 rows: its up half)
             dma_line(rsrc_b, kt == half_kt && c >= 64 ? kPastEnd : row_b + (kd + step * (uint32_t)K) + c,
-                     lds_ring + u * S::kStageBytes + (BM + grp * 8) * kStageK);
+                     lds_ring + u * S::kStageBytes + (S::BM + grp * 8) * kStageK);
         } else {
             dma4(sa_ptr + (int64_t)kt * a.ld_sa, lds_sa + (u * S::kSa + 64 * wave % S::kSa) * 4);
         }
@@ -213,8 +178,8 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
     const int fr = lane & 15;
     const uint32_t f_lo = fr * kStageK + (((lane >> 4) ^ (fr >> 1)) & 7) * 16;
     uint32_t at_x[2] = {lds_ring + wm * kWaveM * kStageK + f_lo, lds_ring + wm * kWaveM * kStageK + (f_lo ^ 64)};
-    uint32_t at_w[2] = {at_x[0] + (BM + wn * kWaveN - wm * kWaveM) * kStageK,
-                        at_x[1] + (BM + wn * kWaveN - wm * kWaveM) * kStageK};
+    uint32_t at_w[2] = {at_x[0] + (S::BM + wn * kWaveN - wm * kWaveM) * kStageK,
+                        at_x[1] + (S::BM + wn * kWaveN - wm * kWaveM) * kStageK};
     uint32_t at_sa = lds_sa + (wm * kWaveM + fr) * 4;
     int other = 1;
     auto flip = [&]() {
@@ -316,52 +281,90 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
     wait_vmcnt<0>();  // the loads past the last stage have landed too
 
     // ---- results: lane l holds channels 4 (l / 16) .. + 3 of each 16-channel
-    // tile for token row l % 16 of each 16-row tile
+    // tile for token row l % 16 of each 16-row tile.  They leave through LDS (the
+    // ring, free now) as whole 16-byte pieces of rows.
     const int cq = (lane >> 4) * 4;
-    if constexpr (MODE == kDense) {
-        uint16_t* Y = a.Y + (size_t)row0 * a.N;
+    __syncthreads();  // every wave's loads and reads of the ring are done
+    if constexpr (MODE != kGateUp) {
+        // 16-bit values of the wave's 64 channels, 128 bytes per row: piece c of row
+        // r in slot c ^ ((r / 2) % 8)
+        int8_t* stage = ring + wave * kWaveM * 128;
+        auto put = [&](int i, int j, const uint16_t (&y)[4]) {
+            const int piece = (2 * i + (lane >> 5)) ^ (fr >> 1);
+            *reinterpret_cast<uint2*>(stage + (16 * j + fr) * 128 + piece * 16 + ((lane >> 4) & 1) * 8) =
+                make_uint2(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16);
+        };
+        const int n_wave = n0 + wn * kWaveN;
+        if constexpr (MODE == kDense) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int n = n0 + wn * kWaveN + 16 * i + cq;
-            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (a.bias != nullptr)
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (n + v < a.N) b[v] = widen16<BF16>(a.bias[n + v]);
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const int m = wm * kWaveM + 16 * j + fr;
-                if (m >= rows) continue;
-                uint16_t y[4];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) y[v] = narrow16<BF16>(acc[i][j][v] + b[v]);
-                uint16_t* out = Y + (size_t)m * a.N + n;
-                if ((a.N & 3) == 0 && n < a.N) {
-                    *reinterpret_cast<uint2*>(out) = make_uint2(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16);
-                } else {
+            for (int i = 0; i < NT; ++i) {
+                float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (a.bias != nullptr)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        if (n + v < a.N) out[v] = y[v];
+                        if (n_wave + 16 * i + cq + v < a.N) b[v] = widen16<BF16>(a.bias[n_wave + 16 * i + cq + v]);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    uint16_t y[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) y[v] = narrow16<BF16>(acc[i][j][v] + b[v]);
+                    put(i, j, y);
+                }
+            }
+        } else {
+            // a row's 128 channels (two waves) as 16-bit integers of their largest
+            float* red = s_sb;  // [WN][BM], past its use
+            static_assert(S::WN * S::BM <= 2 * kMaxKb, "room for the maxima");
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                float m = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) m = fmaxf(m, fabsf(acc[i][j][v]));
+                m = fmaxf(m, __shfl_xor(m, 16));
+                m = fmaxf(m, __shfl_xor(m, 32));
+                if (lane < 16) red[wn * BM + wm * kWaveM + 16 * j + lane] = m;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const int r = wm * kWaveM + 16 * j + fr;
+                const float m = fmaxf(red[(wn & 2) * BM + r], red[((wn & 2) + 1) * BM + r]);
+                const float f = m == 0.0f ? 0.0f : fminf(kPartMax / m, 3.402823466e38f);
+                if ((wn & 1) == 0 && lane < 16 && r < rows && n_wave < a.N)
+                    a.part_scale[(int64_t)(n_wave / kBlock) * a.ld_part + row0 + r] = m * (1.0f / kPartMax);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    uint16_t y[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) y[v] = (uint16_t)(int16_t)__builtin_rintf(acc[i][j][v] * f);
+                    put(i, j, y);
                 }
             }
         }
-    } else if constexpr (MODE == kDown) {
+        wave_fence();
+        uint16_t* Y = (MODE == kDense ? a.Y : a.part) + (size_t)(row0 + wm * kWaveM) * a.N + n_wave;
+        const int piece = lane & 7;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int n = n0 + wn * kWaveN + 16 * i + cq;
+        for (int it = 0; it < 2 * MT; ++it) {
+            const int r = 8 * it + (lane >> 3);
+            if (wm * kWaveM + r >= rows) continue;
+            const v4i y = *reinterpret_cast<const v4i*>(stage + r * 128 + (piece ^ ((r >> 1) & 7)) * 16);
+            uint16_t* out = Y + (size_t)r * a.N + 8 * piece;
+            if ((a.N & 7) == 0) {
+                if (n_wave + 8 * piece < a.N) *reinterpret_cast<v4i*>(out) = y;
+            } else {
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const int m = wm * kWaveM + 16 * j + fr;
-                if (m < rows && n < a.N)  // (N is a multiple of 64)
-                    *reinterpret_cast<v4f*>(a.part + (size_t)(row0 + m) * a.N + n) = acc[i][j];
+                for (int v = 0; v < 8; ++v)
+                    if (n_wave + 8 * piece + v < a.N) out[v] = (uint16_t)((uint32_t)y[v >> 1] >> (16 * (v & 1)));
             }
         }
     } else {
         // h of 32 channels per wave; a row's maximum over the tile's 128
         // channels from the four waves that share its rows
-        static_assert(MODE != kGateUp || (NT == 4 && S::WN == 4), "gate and up of 32 channels per wave");
-        float* red = reinterpret_cast<float*>(ring);  // [WN][BM]
-        __syncthreads();  // every wave's loads and reads of the ring are done
+        float* red = s_sb;  // [WN][BM], past its use
+        int8_t* stage = ring;  // [BM] rows of 128 codes
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             float m = 0.0f;
@@ -370,8 +373,7 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
                 const bool in = n0 + wn * 32 + 16 * i + cq < a.N;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float g = acc[i][j][v], u = acc[i + NT / 2][j][v];
-                    const float h = in ? silu(g) * u : 0.0f;
+                    const float h = in ? silu(acc[i][j][v]) * acc[i + NT / 2][j][v] : 0.0f;
                     acc[i][j][v] = h;
                     m = fmaxf(m, fabsf(h));
                 }
@@ -386,22 +388,78 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
             const int r = wm * kWaveM + 16 * j + fr;
             const float m = fmaxf(fmaxf(red[r], red[BM + r]), fmaxf(red[2 * BM + r], red[3 * BM + r]));
             const float f = block_factor(m);
-            if (r >= rows) continue;
-            if (wn == 0 && lane < 16) a.SH[(int64_t)(n0 / kBlock) * a.ld_sh + row0 + r] = m;
+            if (wn == 0 && lane < 16 && r < rows) a.SH[(int64_t)(n0 / kBlock) * a.ld_sh + row0 + r] = m;
 #pragma unroll
-            for (int i = 0; i < NT / 2; ++i) {
-                const int n = n0 + wn * 32 + 16 * i + cq;
-                if (n < a.N)
-                    *reinterpret_cast<uint32_t*>(a.H + (size_t)(row0 + r) * a.N + n) =
-                        e4m3_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], f);
-            }
+            for (int i = 0; i < NT / 2; ++i)
+                *reinterpret_cast<uint32_t*>(stage + r * 128 + ((2 * wn + i) ^ (fr >> 1)) * 16 + cq) =
+                    e4m3_pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3], f);
+        }
+        __syncthreads();
+        uint8_t* H = a.H + (size_t)row0 * a.N + n0;
+        for (int o = tid; o < BM * 8; o += 64 * S::NW) {
+            const int r = o >> 3, piece = o & 7;
+            if (r < rows && n0 + 16 * piece < a.N)  // (N is a multiple of 64)
+                *reinterpret_cast<v4i*>(H + (size_t)r * a.N + 16 * piece) =
+                    *reinterpret_cast<const v4i*>(stage + r * 128 + (piece ^ ((r >> 1) & 7)) * 16);
         }
     }
 }
 
-typedef Shape<256, 2, 4> Tile256;
-typedef Shape<128, 2, 4> Tile128;
-typedef Shape<32, 1, 4> Tile32;
+template <typename S, int MODE, bool BF16>
+__global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a) {
+    __shared__ __align__(1024) int8_t ring[2 * S::kStageBytes];
+    __shared__ float s_sa[2 * S::kSa];
+    __shared__ float s_sb[2 * kMaxKb];
+    constexpr int chans = MODE == kGateUp ? S::BN / 2 : S::BN;  // output channels of a tile
+    const int tiles_n = (a.N + chans - 1) / chans;
+    Tile t;
+    if constexpr (MODE == kDense) {
+        constexpr int kGroupM = 4;  // tile rows that share a weight panel in L2
+        const int tiles_m = (int)(((int64_t)a.M + a.tile_rows - 1) / a.tile_rows);
+        const int L = xcd_order(blockIdx.x, tiles_m * tiles_n);
+        const int first = L / (kGroupM * tiles_n) * kGroupM;
+        const int gsz = min(tiles_m - first, kGroupM), in = L - first * tiles_n;
+        t.row0 = (first + in % gsz) * a.tile_rows;
+        t.n0 = in / gsz * chans;
+        t.rows = min(a.tile_rows, a.M - t.row0);
+        t.e = 0;
+    } else {
+        const int total = a.tiles[0] * tiles_n;
+        if ((int)blockIdx.x >= total) return;
+        const int L = xcd_order(blockIdx.x, total);
+        const int32_t* at = a.tiles + 4 + 4 * (L / tiles_n);
+        t.e = __builtin_amdgcn_readfirstlane(at[0]);
+        t.row0 = __builtin_amdgcn_readfirstlane(at[1]);
+        t.rows = __builtin_amdgcn_readfirstlane(at[2]);
+        t.n0 = L % tiles_n * chans;
+    }
+    // weight block scales of the tile's two 128-channel halves (gate and up, or
+    // channels n0.. and n0 + 128..), with the codes' 1/448^2
+    const int nkb = (a.K + kBlock - 1) / kBlock, nnb = (a.N + kBlock - 1) / kBlock;
+    const float* sb0 = a.SCB + ((size_t)t.e * (MODE == kGateUp ? 2 : 1) * nnb + t.n0 / kBlock) * nkb;
+    const float* sb1 = MODE == kGateUp ? sb0 + (size_t)nnb * nkb : t.n0 + kBlock < a.N ? sb0 + nkb : sb0;
+    for (int i = threadIdx.x; i < nkb; i += 64 * S::NW) {
+        s_sb[i] = sb0[i] * kCodeScale;
+        s_sb[kMaxKb + i] = sb1[i] * kCodeScale;
+    }
+    // as few row tiles per wave as the rows need
+    constexpr int kRows = 16 * S::WM;
+    if constexpr (S::kMaxMT == 8) {
+        if (t.rows > 6 * kRows)
+            tile_body<S, MODE, BF16, 8>(a, t, ring, s_sa, s_sb);
+        else if (t.rows > 4 * kRows)
+            tile_body<S, MODE, BF16, 6>(a, t, ring, s_sa, s_sb);
+        else if (t.rows > 2 * kRows)
+            tile_body<S, MODE, BF16, 4>(a, t, ring, s_sa, s_sb);
+        else
+            tile_body<S, MODE, BF16, 2>(a, t, ring, s_sa, s_sb);
+    } else {
+        tile_body<S, MODE, BF16, S::kMaxMT>(a, t, ring, s_sa, s_sb);
+    }
+}
+
+typedef Shape<2, 4, 8> TileBig;    // up to 256 rows, 8 waves
+typedef Shape<1, 4, 2> TileSmall;  // up to 32 rows, 4 waves
 
 template <typename S, int MODE>
 hipError_t launch(const BlockGemmArgs& a, int64_t tiles_m, hipStream_t stream) {
@@ -415,55 +473,58 @@ hipError_t launch(const BlockGemmArgs& a, int64_t tiles_m, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Rows of a dense product's tiles: 64, 128, 192 or 256, whichever takes the least
+// time in rounds of the 256 CUs.  A tile's K stage is bound by LDS traffic: the
+// weights' 96 KiB (written once, read by both wave rows) and 40 KiB for each 64
+// rows.
+int dense_tile_rows(int64_t M, int64_t N) {
+    const int64_t tiles_n = (N + TileBig::BN - 1) / TileBig::BN;
+    int best = 256;
+    int64_t least = INT64_MAX;
+    for (int rows = 256; rows >= 64; rows -= 64) {
+        const int64_t rounds = ((M + rows - 1) / rows * tiles_n + 255) / 256;
+        const int64_t time = rounds * (96 + 40 * (rows / 64));
+        if (time < least) {
+            least = time;
+            best = rows;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 size_t gemm_block_workspace(int64_t, int64_t, int64_t) { return 0; }
 
-namespace {
-
-// Row blocks of the activations small enough for one launch's grid.
-template <typename S>
-hipError_t launch_dense(BlockGemmArgs a, hipStream_t stream) {
-    const int64_t tiles_n = ((int64_t)a.N + S::BN - 1) / S::BN;
-    const int64_t most = kMaxGrid / tiles_n * S::BM, all = a.M;
-    const uint8_t* CA = a.CA;
-    const float* SCA = a.SCA;
-    uint16_t* Y = a.Y;
-    for (int64_t m = 0; m < all; m += most) {
-        a.M = (int)(all - m < most ? all - m : most);
-        a.CA = CA + m * a.K;
-        a.SCA = SCA + m;
-        a.Y = Y + m * a.N;
-        const hipError_t e = launch<S, kDense>(a, ((int64_t)a.M + S::BM - 1) / S::BM, stream);
+hipError_t launch_gemm_block(const BlockGemmArgs& in, void* workspace, hipStream_t stream) {
+    (void)workspace;
+    if (gemm_block_streams(in.M, in.N, in.K)) return launch_gemm_block_stream(in, stream);
+    BlockGemmArgs a = in;
+    a.tile_rows = dense_tile_rows(in.M, in.N);
+    // row blocks of the activations small enough for one launch's grid
+    const int64_t tiles_n = ((int64_t)a.N + TileBig::BN - 1) / TileBig::BN;
+    const int64_t most = kMaxGrid / tiles_n * a.tile_rows;
+    for (int64_t m = 0; m < in.M; m += most) {
+        a.M = (int)(in.M - m < most ? in.M - m : most);
+        a.CA = in.CA + m * a.K;
+        a.SCA = in.SCA + m;
+        a.Y = in.Y + m * a.N;
+        const hipError_t e = launch<TileBig, kDense>(a, ((int64_t)a.M + a.tile_rows - 1) / a.tile_rows, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
-}  // namespace
-
-hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, hipStream_t stream) {
-    (void)workspace;
-    if (gemm_block_streams(a.M, a.N, a.K)) return launch_gemm_block_stream(a, stream);
-    if (a.M > 512) return launch_dense<Tile256>(a, stream);
-    return launch_dense<Tile128>(a, stream);
-}
-
-int grouped_tile_rows(int64_t pairs, int E) {
-    const int64_t mean = pairs / E;
-    return mean > 256 ? 256 : mean > 48 ? 128 : 32;
-}
+int grouped_tile_rows(int64_t pairs, int E) { return pairs / E > 48 ? TileBig::BM : TileSmall::BM; }
 
 hipError_t launch_experts_gate_up(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
-    if (tile_rows == 256) return launch<Tile256, kGateUp>(a, max_tiles, stream);
-    if (tile_rows == 128) return launch<Tile128, kGateUp>(a, max_tiles, stream);
-    return launch<Tile32, kGateUp>(a, max_tiles, stream);
+    if (tile_rows == TileBig::BM) return launch<TileBig, kGateUp>(a, max_tiles, stream);
+    return launch<TileSmall, kGateUp>(a, max_tiles, stream);
 }
 
 hipError_t launch_experts_down(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
-    if (tile_rows == 256) return launch<Tile256, kDown>(a, max_tiles, stream);
-    if (tile_rows == 128) return launch<Tile128, kDown>(a, max_tiles, stream);
-    return launch<Tile32, kDown>(a, max_tiles, stream);
+    if (tile_rows == TileBig::BM) return launch<TileBig, kDown>(a, max_tiles, stream);
+    return launch<TileSmall, kDown>(a, max_tiles, stream);
 }
 
 }  // namespace llmint8
