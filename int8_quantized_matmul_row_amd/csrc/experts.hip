@@ -28,41 +28,74 @@ __device__ __forceinline__ int block_excl_scan(int v, int* waves, int* total) {
     return before + incl - v;
 }
 
-// One workgroup: counts the pairs of each expert, lays the experts' rows out
-// one after another, gives every pair its row (in no particular order within
-// an expert: a row's results do not depend on its place) and lists the tiles:
-// as few of at most `tile_rows` rows as hold an expert's, of even size in units
-// of `unit` rows.  Pairs whose id is outside [0, E) get row -1.
-__global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
-                                                                  int top_k, int E, int tile_rows, int unit,
-                                                                  int32_t* __restrict__ pair_row,
-                                                                  int32_t* __restrict__ row_token,
-                                                                  int32_t* __restrict__ tiles) {
-    __shared__ int count[kMaxExperts], next[kMaxExperts], waves[kSortThreads / 64];
+// The pairs are sorted by expert in two passes over equal parts of the pairs, one
+// workgroup each: every part's counts, then its rows.
+__global__ __launch_bounds__(kSortThreads) void count_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
+                                                                   int per_part, int E,
+                                                                   int32_t* __restrict__ counts) {
+    __shared__ int count[kMaxExperts];
     const int tid = threadIdx.x;
     count[tid] = 0;
     __syncthreads();
-    for (int p = tid; p < pairs; p += kSortThreads) {
+    const int end = min(pairs, (int)(blockIdx.x + 1) * per_part);
+    for (int p = blockIdx.x * per_part + tid; p < end; p += kSortThreads) {
         const int e = ids[p];
         if ((uint32_t)e < (uint32_t)E) atomicAdd(&count[e], 1);
     }
     __syncthreads();
-    const int c = count[tid];
+    if (tid < E) counts[blockIdx.x * E + tid] = count[tid];
+}
+
+// Lays the experts' rows out one after another and gives every pair of the
+// workgroup's part its row (in no particular order within an expert and part: a
+// row's results do not depend on its place); pairs whose id is outside [0, E)
+// get row -1.  The first workgroup lists the tiles: as few of at most
+// `tile_rows` rows as hold an expert's, of even size in units of `unit` rows.
+// counts == nullptr: one part, counted here.
+__global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
+                                                                  int per_part, int top_k, int E, int tile_rows,
+                                                                  int unit, const int32_t* __restrict__ counts,
+                                                                  int32_t* __restrict__ pair_row,
+                                                                  int32_t* __restrict__ row_token,
+                                                                  int32_t* __restrict__ tiles) {
+    __shared__ int next[kMaxExperts], waves[kSortThreads / 64];
+    const int tid = threadIdx.x, part = blockIdx.x;
+    int c = 0, before = 0;  // the expert's rows, and those of earlier parts
+    if (counts != nullptr) {
+        if (tid < E)
+            for (int g = 0; g < (int)gridDim.x; ++g) {
+                const int n = counts[g * E + tid];
+                before += g < part ? n : 0;
+                c += n;
+            }
+    } else {
+        next[tid] = 0;
+        __syncthreads();
+        for (int p = tid; p < pairs; p += kSortThreads) {
+            const int e = ids[p];
+            if ((uint32_t)e < (uint32_t)E) atomicAdd(&next[e], 1);
+        }
+        __syncthreads();
+        c = next[tid];
+    }
     int total;
     const int first = block_excl_scan(c, waves, &total);
-    next[tid] = first;
-    const int nt = (c + tile_rows - 1) / tile_rows;
-    const int t0 = block_excl_scan(nt, waves, &total);
-    if (tid == 0) tiles[0] = total;
-    const int step = nt > 0 ? ((c + unit - 1) / unit + nt - 1) / nt * unit : 0;
-    for (int t = 0; t < nt; ++t) {
-        int32_t* out = tiles + 4 + 4 * (t0 + t);
-        out[0] = tid;
-        out[1] = first + t * step;
-        out[2] = min(step, c - t * step);
+    if (part == 0) {  // (uniform)
+        const int nt = (c + tile_rows - 1) / tile_rows;
+        const int t0 = block_excl_scan(nt, waves, &total);
+        if (tid == 0) tiles[0] = total;
+        const int step = nt > 0 ? ((c + unit - 1) / unit + nt - 1) / nt * unit : 0;
+        for (int t = 0; t < nt; ++t) {
+            int32_t* out = tiles + 4 + 4 * (t0 + t);
+            out[0] = tid;
+            out[1] = first + t * step;
+            out[2] = min(step, c - t * step);
+        }
     }
+    next[tid] = first + before;
     __syncthreads();
-    for (int p = tid; p < pairs; p += kSortThreads) {
+    const int end = min(pairs, (part + 1) * per_part);
+    for (int p = part * per_part + tid; p < end; p += kSortThreads) {
         const int e = ids[p];
         int row = -1;
         if ((uint32_t)e < (uint32_t)E) {
@@ -71,6 +104,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
         }
         pair_row[p] = row;
     }
+}
+
+// Parts of the two-pass sort.  Up to 2048 pairs one workgroup does it all in one
+// launch (270 pairs 3 us; 32768 pairs 31 us in one workgroup).
+int sort_parts(int64_t pairs) {
+    if (pairs <= 2 * kSortThreads) return 1;
+    const int64_t parts = (pairs + 2 * kSortThreads - 1) / (2 * kSortThreads);
+    return (int)(parts < 64 ? parts : 64);
 }
 
 // Y[t, :] = sum_j w[t, j] * part[row(t, j), :] * part_scale, in fp32 and in the
@@ -111,7 +152,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const int16_t* __restrict_
 // A chunk of tokens and its share of the workspace.
 struct ExpertsLayout {
     int64_t tokens;  // of a chunk
-    size_t ca, sca, pair_row, row_token, tiles, h, sh, part, part_scale, total;
+    size_t ca, sca, counts, pair_row, row_token, tiles, h, sh, part, part_scale, total;
 };
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -140,6 +181,7 @@ ExpertsLayout layout(int64_t T, int E, int top_k, int K, int I) {
     };
     L.ca = take((size_t)n * K);
     L.sca = take((size_t)nkb * n * 4);
+    L.counts = take((size_t)sort_parts(P) * E * 4);
     L.pair_row = take((size_t)P * 4);
     L.row_token = take((size_t)P * 4);
     L.tiles = take(16 + 16 * (size_t)max_tiles(P, E, 32));
@@ -179,9 +221,14 @@ hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t str
         float* part_scale = reinterpret_cast<float*>(ws + L.part_scale);
         hipError_t e = launch_quantize_act_block(a.X + (size_t)t0 * a.K, a.bf16, n, a.K, ca, sca, stream);
         if (e != hipSuccess) return e;
-        sort_pairs_kernel<<<1, kSortThreads, 0, stream>>>(a.ids + t0 * a.top_k, P, a.top_k, a.E, tile_rows,
-                                                          tile_rows < 64 ? tile_rows : 64, pair_row,
-                                                          row_token, tiles);
+        const int parts = sort_parts(P), per_part = (P + parts - 1) / parts;
+        int32_t* counts = parts > 1 ? reinterpret_cast<int32_t*>(ws + L.counts) : nullptr;
+        const int32_t* ids = a.ids + t0 * a.top_k;
+        if (parts > 1)
+            count_pairs_kernel<<<parts, kSortThreads, 0, stream>>>(ids, P, per_part, a.E, counts);
+        sort_pairs_kernel<<<parts, kSortThreads, 0, stream>>>(ids, P, per_part, a.top_k, a.E, tile_rows,
+                                                              tile_rows < 64 ? tile_rows : 64, counts, pair_row,
+                                                              row_token, tiles);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         BlockGemmArgs g;
         g.bf16 = a.bf16;

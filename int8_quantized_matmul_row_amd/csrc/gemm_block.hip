@@ -40,17 +40,17 @@ __device__ __forceinline__ v4f mfma_block(const v8i& w, const v8i& x) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0);
 }
 
-// lane p's 4 bytes at gptr land in LDS at lds_addr + 4 p
-__device__ __forceinline__ void dma4(const float* gptr, uint32_t lds_addr) {
+// lane p's 4 bytes at base + off land in LDS at lds_addr + 4 p
+__device__ __forceinline__ void dma4(const float* base, uint32_t off, uint32_t lds_addr) {
     uint32_t saved;
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %1\n\t"
         "s_nop 0\n\t"
-        "global_load_lds_dword %2, off\n\t"
+        "global_load_lds_dword %2, %3\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)
-        : "s"(lds_addr), "v"(gptr)
+        : "s"(lds_addr), "v"(off), "s"(base)
         : "memory");
 }
 
@@ -134,14 +134,12 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
     }
     row_b *= (uint32_t)K;
     // the row scales: lane p of each instruction one row of 64
-    const float* sa_ptr;
+    uint32_t sa_off;
     {
         const int r = min((64 * wave + lane) % S::kSa, rows - 1);
-        if constexpr (MODE == kGateUp)
-            sa_ptr = a.SCA + a.row_token[row0 + r];
-        else
-            sa_ptr = a.SCA + row0 + r;
+        sa_off = 4 * (uint32_t)(MODE == kGateUp ? a.row_token[row0 + r] : r);
     }
+    const float* sa_base = MODE == kGateUp ? a.SCA : a.SCA + row0;
     const uint32_t lds_ring = __builtin_amdgcn_readfirstlane(lds_address(ring));
     const uint32_t lds_sa = __builtin_amdgcn_readfirstlane(lds_address(reinterpret_cast<const int8_t*>(s_sa)));
     const int half_kt = K % kStageK != 0 ? nkb - 1 : -1;  // the stage whose second half is past K
@@ -157,8 +155,7 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
             const uint32_t c = ch ^ ((uint32_t)((kDmaA % 2 == 0 ? d : wave + d) & 1) << 6);
             const uint32_t row = MODE == kGateUp ? row_a[MODE == kGateUp ? d : 0] + kd
                                                  : row_a[0] + (kd + (uint32_t)(8 * d) * (uint32_t)K);
-            dma_line(rsrc_a, kt == half_kt && c >= 64 ? kPastEnd : row + c,
-                     lds_ring + u * S::kStageBytes + grp * 8 * kStageK);
+            dma_line(rsrc_a, kt == half_kt && c >= 64 ? kPastEnd : row + c, lds_ring + u * S::kStageBytes + grp * 8 * kStageK);
         } else if (d < kDmaA + kDmaB) {
             const int i = d - kDmaA, grp = kDmaB * wave + i;
             const uint32_t c = ch ^ ((uint32_t)(i & 1) << 6);
@@ -167,7 +164,7 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
             dma_line(rsrc_b, kt == half_kt && c >= 64 ? kPastEnd : row_b + (kd + step * (uint32_t)K) + c,
                      lds_ring + u * S::kStageBytes + (S::BM + grp * 8) * kStageK);
         } else {
-            dma4(sa_ptr + (int64_t)kt * a.ld_sa, lds_sa + (u * S::kSa + 64 * wave % S::kSa) * 4);
+            dma4(sa_base + (int64_t)kt * a.ld_sa, sa_off, lds_sa + (u * S::kSa + 64 * wave % S::kSa) * 4);
         }
     };
 
@@ -266,6 +263,17 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
     // before it would have loaded
 #pragma unroll
     for (int d = 0; d < kDma; ++d) dma(d, 0, 0);
+    // meanwhile the weight block scales of the tile's two 128-channel halves (gate
+    // and up, or channels n0.. and n0 + 128..), with the codes' 1/448^2
+    {
+        const int nnb = (a.N + kBlock - 1) / kBlock;
+        const float* sb_lo = a.SCB + ((size_t)e * (MODE == kGateUp ? 2 : 1) * nnb + n0 / kBlock) * nkb;
+        const float* sb_hi = MODE == kGateUp ? sb_lo + (size_t)nnb * nkb : n0 + kBlock < a.N ? sb_lo + nkb : sb_lo;
+        for (int i = tid; i < nkb; i += 64 * S::NW) {
+            s_sb[i] = sb_lo[i] * kCodeScale;
+            s_sb[kMaxKb + i] = sb_hi[i] * kCodeScale;
+        }
+    }
     __builtin_amdgcn_s_waitcnt(0);
     stage_barrier();
 #pragma unroll
@@ -353,7 +361,9 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
             const v4i y = *reinterpret_cast<const v4i*>(stage + r * 128 + (piece ^ ((r >> 1) & 7)) * 16);
             uint16_t* out = Y + (size_t)r * a.N + 8 * piece;
             if ((a.N & 7) == 0) {
-                if (n_wave + 8 * piece < a.N) *reinterpret_cast<v4i*>(out) = y;
+                // non-temporal: written once, past the caches that hold the operands
+                // (4096 x 28672 x 8192 794 -> 788 us)
+                if (n_wave + 8 * piece < a.N) __builtin_nontemporal_store(y, reinterpret_cast<v4i*>(out));
             } else {
 #pragma unroll
                 for (int v = 0; v < 8; ++v)
@@ -432,15 +442,6 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
         t.row0 = __builtin_amdgcn_readfirstlane(at[1]);
         t.rows = __builtin_amdgcn_readfirstlane(at[2]);
         t.n0 = L % tiles_n * chans;
-    }
-    // weight block scales of the tile's two 128-channel halves (gate and up, or
-    // channels n0.. and n0 + 128..), with the codes' 1/448^2
-    const int nkb = (a.K + kBlock - 1) / kBlock, nnb = (a.N + kBlock - 1) / kBlock;
-    const float* sb0 = a.SCB + ((size_t)t.e * (MODE == kGateUp ? 2 : 1) * nnb + t.n0 / kBlock) * nkb;
-    const float* sb1 = MODE == kGateUp ? sb0 + (size_t)nnb * nkb : t.n0 + kBlock < a.N ? sb0 + nkb : sb0;
-    for (int i = threadIdx.x; i < nkb; i += 64 * S::NW) {
-        s_sb[i] = sb0[i] * kCodeScale;
-        s_sb[kMaxKb + i] = sb1[i] * kCodeScale;
     }
     // as few row tiles per wave as the rows need
     constexpr int kRows = 16 * S::WM;
