@@ -564,7 +564,7 @@ llmint8_status llmint8_matmul_fp8_block(int dtype, int64_t M, int64_t N, int64_t
     llmint8::BlockGemmArgs a = block_gemm_args(dtype, M, N, K, CB, SCB, bias, Y);
     a.CA = CA;
     a.SCA = SCA;
-    hipError_t e = llmint8::launch_gemm_block(a, workspace, stream);
+    hipError_t e = llmint8::launch_gemm_block(a, workspace, false, stream);
     return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
 }
 
@@ -595,11 +595,14 @@ llmint8_status llmint8_linear_fp8_block(const void* X, int dtype, int64_t M, int
     char* ws = static_cast<char*>(workspace);
     uint8_t* ca = reinterpret_cast<uint8_t*>(ws);
     float* sca = reinterpret_cast<float*>(ws + L.sca);
-    hipError_t e = llmint8::launch_quantize_act_block(X, a.bf16, a.M, a.K, ca, sca, stream);
+    // (a split product's arrival counters start its workspace: cleared on the way)
+    hipError_t e = llmint8::launch_quantize_act_block(X, a.bf16, a.M, a.K, ca, sca, stream,
+                                                      reinterpret_cast<uint32_t*>(ws + L.end),
+                                                      llmint8::gemm_block_counters(M, N, K));
     if (e != hipSuccess) return hip_fail(e);
     a.CA = ca;
     a.SCA = sca;
-    e = llmint8::launch_gemm_block(a, ws + L.end, stream);
+    e = llmint8::launch_gemm_block(a, ws + L.end, true, stream);
     return e == hipSuccess ? LLMINT8_OK : hip_fail(e);
 }
 

@@ -591,8 +591,9 @@ hipError_t launch_linear_decode(const void* X, bool bf16, bool fp8, int M, int N
                                 hipEvent_t ev_start, hipEvent_t ev_stop);
 
 // ---- block-scaled FP8 launchers ------------------------------------------------
+// clear: n_clear words set to 0 on the way
 hipError_t launch_quantize_act_block(const void* X, bool bf16, int M, int K, uint8_t* CA, float* SCA,
-                                     hipStream_t stream);
+                                     hipStream_t stream, uint32_t* clear = nullptr, int n_clear = 0);
 hipError_t launch_quantize_weight_block(const void* W, bool bf16, int64_t batch, int N, int K, uint8_t* CB,
                                         float* SCB, hipStream_t stream);
 
@@ -635,11 +636,20 @@ struct BlockGemmArgs {
     uint16_t* part = nullptr;     // [rows, N] 16-bit integers, row r's block b
     float* part_scale = nullptr;  // times part_scale[b * ld_part + r]
     int64_t ld_part = 0;
-    int tile_rows = 0;  // dense tiles: set by the launcher
+    // dense tiles, set by the launcher: rows of a tile, workgroups that share a
+    // tile's K, their counters and parts
+    int tile_rows = 0, split = 1, split_tiles = 0;
+    void* split_ws = nullptr;
 };
+// A split product's workspace starts with one arrival counter per tile, which
+// start at 0: cleared by launch_gemm_block, or ahead of it by the activation
+// quantizer (counters_cleared).
+constexpr int kBlockSplitMax = 16;
+__host__ __device__ inline size_t split_counter_bytes(int tiles) { return ((size_t)tiles * 4 + 255) & ~(size_t)255; }
 size_t gemm_block_workspace(int64_t M, int64_t N, int64_t K);
-hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, hipStream_t stream);
-bool gemm_block_streams(int64_t M, int64_t N, int64_t K);
+int gemm_block_counters(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_block(const BlockGemmArgs& a, void* workspace, bool counters_cleared, hipStream_t stream);
+int64_t gemm_block_stream_time(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_block_stream(const BlockGemmArgs& a, hipStream_t stream);
 bool linear_block_fused(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_block_fused(const BlockGemmArgs& a, const void* X, hipStream_t stream);

@@ -62,19 +62,74 @@ __device__ __forceinline__ int xcd_order(int b, int total) {
 }
 
 // A workgroup's waves stand WM x WN on its tile; every wave has NT = 4 channel
-// tiles of 16 and up to kMaxMT row tiles of 16.
-template <int WM_, int WN_, int kMaxMT_>
+// tiles of 16 (half a weight block, or gate and up of 32 channels) and up to
+// kMaxMT row tiles of 16.  The ring holds kStages K stages.  kSplit: several
+// workgroups may share a dense tile's K.
+template <int WM_, int WN_, int kMaxMT_, int kStages_, bool kSplit_ = false>
 struct Shape {
-    static constexpr int WM = WM_, WN = WN_, NW = WM * WN, kMaxMT = kMaxMT_;
-    static constexpr int BM = 16 * WM * kMaxMT, BN = 256, NT = BN / WN / 16;
+    static constexpr bool kSplit = kSplit_;
+    static constexpr int WM = WM_, WN = WN_, NW = WM * WN, kMaxMT = kMaxMT_, kStages = kStages_;
+    static constexpr int NT = 4, BM = 16 * WM * kMaxMT, BN = 16 * NT * WN;
     static constexpr int kStageBytes = (BM + BN) * kStageK;
-    static constexpr int kSa = BM < 64 ? 64 : BM;  // floats of a stage's row scales
-    static_assert(NT == 4 && WN == 4, "a wave's 64 channels: half a weight block, or gate and up of 32");
+    static constexpr int kSa = BM < 64 ? 64 : BM;       // floats of a stage's row scales
+    static constexpr int kHalves = BN / kBlock;         // weight blocks (gate and up: 2)
+    static_assert(BN % kBlock == 0 && kHalves <= 2, "whole weight blocks");
 };
 
 struct Tile {
     int row0, rows, n0, e;  // rows [row0, row0 + rows), channels from n0 of weight matrix e
+    int kb0, nkb;           // K blocks [kb0, kb0 + nkb)
+    int part, index;        // which of the split's parts, the tile's number (split K)
 };
+
+// ---- split K: the partial sums of a tile's workgroups meet in the workspace ----
+// In register order, 16 bytes per lane, so that every access is a full 1 KiB.
+// Stores and the last arriver's loads are device-coherent (sc1: written through,
+// read past a stale L2 line), so no fence has to write back or invalidate an
+// XCD's L2: the stores complete (vmcnt) before the arrival count, the loads
+// follow it.  Returns whether this workgroup finishes the tile (the last to
+// arrive); it then holds the sum of all parts in their order, its own read back
+// too: the same result whichever comes last.  mine: the wave has rows of the tile.
+template <int NW, int NT, int MT>
+__device__ __forceinline__ bool split_sum(v4f (&acc)[NT][MT], const Tile& t, int split, void* ws, int tiles,
+                                          bool mine, int wave, int lane, float* s_last) {
+    constexpr int kCoherent = 16;                      // cache policy sc1: device scope
+    constexpr int kTileBytes = NW * NT * MT * 64 * 16;
+    uint32_t* counters = static_cast<uint32_t*>(ws);
+    char* parts = static_cast<char*>(ws) + split_counter_bytes(tiles);
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        parts + (size_t)t.index * split * kTileBytes, 0, split * kTileBytes, 0x00020000);
+    auto at = [&](int part, int i, int j) {
+        return part * kTileBytes + ((wave * NT + i) * MT + j) * 1024 + lane * 16;
+    };
+    if (mine)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, acc[i][j]), rsrc, at(t.part, i, j), 0,
+                                                       kCoherent);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part is stored device-wide
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *s_last = atomicAdd(counters + t.index, 1u) == (unsigned)(split - 1) ? 1.0f : 0.0f;
+    __syncthreads();
+    if (*s_last == 0.0f) return false;
+    if (mine) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int p = 0; p < split; ++p)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    acc[i][j] += __builtin_bit_cast(
+                        v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at(p, i, j), 0, kCoherent));
+    }
+    return true;
+}
 
 // The tile's work with MT row tiles per wave (rows <= 16 WM MT).
 template <typename S, int MODE, bool BF16, int MT>
@@ -86,7 +141,7 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
-    const int K = a.K, nkb = (K + kBlock - 1) / kBlock;
+    const int K = a.K, nkb = tile.nkb, kb0 = S::kSplit ? tile.kb0 : 0;
     const int row0 = tile.row0, rows = tile.rows, n0 = tile.n0, e = tile.e;
 
     // ---- stage loads: one instruction = 8 rows x 128 bytes; lane p fills slot
@@ -142,14 +197,17 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
     const float* sa_base = MODE == kGateUp ? a.SCA : a.SCA + row0;
     const uint32_t lds_ring = __builtin_amdgcn_readfirstlane(lds_address(ring));
     const uint32_t lds_sa = __builtin_amdgcn_readfirstlane(lds_address(reinterpret_cast<const int8_t*>(s_sa)));
-    const int half_kt = K % kStageK != 0 ? nkb - 1 : -1;  // the stage whose second half is past K
+    // the stage whose second half is past K
+    const int half_kt = K % kStageK != 0 && (kb0 + nkb) * kStageK > K ? nkb - 1 : -1;
     // load d of a wave's kDma per stage: A rows, B rows, the row scales.  Past
-    // the last stage it re-reads that one, into a buffer nobody reads again.
+    // the last stage, into buffers nobody reads again, it reads past the tile's
+    // rows (at most 2^31 bytes: 0, no traffic) or, where the buffer is all of the
+    // tokens or of an expert, the last stage again.
     constexpr int kDma = kDmaA + kDmaB + 1;
     static_assert(kDmaB % 2 == 0, "parity of the 8-row groups");
     auto dma = [&](int d, int kt_want, int u) {
         const int kt = min(kt_want, nkb - 1);
-        const uint32_t kd = (uint32_t)kt * kStageK;
+        const uint32_t kd = MODE == kGateUp || kt_want < nkb ? (uint32_t)(kb0 + kt) * kStageK : 0x80000000u;
         if (d < kDmaA) {
             const int grp = kDmaA * wave + d;
             const uint32_t c = ch ^ ((uint32_t)((kDmaA % 2 == 0 ? d : wave + d) & 1) << 6);
@@ -164,13 +222,13 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
             dma_line(rsrc_b, kt == half_kt && c >= 64 ? kPastEnd : row_b + (kd + step * (uint32_t)K) + c,
                      lds_ring + u * S::kStageBytes + (S::BM + grp * 8) * kStageK);
         } else {
-            dma4(sa_base + (int64_t)kt * a.ld_sa, sa_off, lds_sa + (u * S::kSa + 64 * wave % S::kSa) * 4);
+            dma4(sa_base + (int64_t)(kb0 + kt) * a.ld_sa, sa_off, lds_sa + (u * S::kSa + 64 * wave % S::kSa) * 4);
         }
     };
 
     // ---- fragments: lane l holds 32 bytes of row (l % 16), chunks l / 16 and
     // l / 16 + 4 (the same K order for both operands).  The addresses of the
-    // wave's first rows in the current buffer; `other` leads to the other one.
+    // wave's first rows in the current buffer.
     constexpr int kWaveM = MT * 16, kWaveN = NT * 16;
     const int fr = lane & 15;
     const uint32_t f_lo = fr * kStageK + (((lane >> 4) ^ (fr >> 1)) & 7) * 16;
@@ -178,14 +236,17 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
     uint32_t at_w[2] = {at_x[0] + (S::BM + wn * kWaveN - wm * kWaveM) * kStageK,
                         at_x[1] + (S::BM + wn * kWaveN - wm * kWaveM) * kStageK};
     uint32_t at_sa = lds_sa + (wm * kWaveM + fr) * 4;
-    int other = 1;
-    auto flip = [&]() {
-        at_x[0] += other * S::kStageBytes;
-        at_x[1] += other * S::kStageBytes;
-        at_w[0] += other * S::kStageBytes;
-        at_w[1] += other * S::kStageBytes;
-        at_sa += other * S::kSa * 4;
-        other = -other;
+    constexpr int kRing = S::kStages;
+    int buf = 0;  // the current stage's buffer
+    auto next_of = [](int u) { return u + 1 == kRing ? 0 : u + 1; };
+    auto advance = [&]() {
+        const int by = next_of(buf) - buf;
+        at_x[0] += by * S::kStageBytes;
+        at_x[1] += by * S::kStageBytes;
+        at_w[0] += by * S::kStageBytes;
+        at_w[1] += by * S::kStageBytes;
+        at_sa += by * S::kSa * 4;
+        buf += by;
     };
     auto frag = [&](const uint32_t (&at)[2], int row) -> v8i {
         const v4i lo = lds_at<v4i>(at[0] + row * kStageK), hi = lds_at<v4i>(at[1] + row * kStageK);
@@ -199,14 +260,16 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
         for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     // which half's weight scale a wave's channel tiles take
     const float* sb_at = s_sb + (MODE == kGateUp ? 0 : wn * kWaveN / kBlock) * kMaxKb;
+    static_assert(MODE != kGateUp || S::kHalves == 2, "gate and up");
 
     // The K loop.  Row tile j's MFMAs fill p[j % 2] while the results of the
     // row tile before are scaled and added; its activations are read one row
-    // tile ahead.  Between the stage's last two row tiles every wave waits for
-    // its loads of the next stage and its reads of this one, and meets the
-    // others: the next stage is in the other buffer, this one is free.  The last
-    // row tile reads the next stage's weights in place, and the loads of the
-    // stage after go out with it and with the first row tile that follows.
+    // tile ahead.  Ahead of the stage's last row tile every wave waits for its
+    // loads of the next stage (those of later stages stay in flight) and its
+    // reads of this one, and meets the others: the next stage is in the next
+    // buffer, this one is free.  The last row tile reads the next stage's weights
+    // in place, and the loads that refill this buffer go out with it and with the
+    // first row tile that follows.
     static_assert(MT % 2 == 0, "the row tiles alternate between two register sets");
     v8i w[NT], x[2];
     v4f p[2][NT];
@@ -225,13 +288,15 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
 #pragma unroll
     for (int i = 0; i < NT; ++i) p[1][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     auto stage = [&](int kt) {
-        const int u = kt & 1;
+        int freed = buf;  // takes stage kt + kRing after the meeting
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             if (j == MT - 1) {
-                __builtin_amdgcn_s_waitcnt(0);
+                wait_vmcnt<(kRing - 2) * kDma>();
+                __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
                 stage_barrier();
-                flip();
+                freed = buf;
+                advance();
                 x[0] = frag(at_x, 0);  // (x[0]'s last use has been issued)
                 sa[0] = read_sa(0);
             } else {
@@ -246,12 +311,12 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
                 add(i, (j + MT - 1) % MT, (j + 1) & 1);
                 if (j == MT - 1)
 #pragma unroll
-                    for (int d = i * (kDma / 2) / NT; d < (i + 1) * (kDma / 2) / NT; ++d) dma(d, kt + 2, u);
+                    for (int d = i * (kDma / 2) / NT; d < (i + 1) * (kDma / 2) / NT; ++d) dma(d, kt + kRing, freed);
                 if (j == 0)
 #pragma unroll
                     for (int d = kDma / 2 + i * (kDma - kDma / 2) / NT;
                          d < kDma / 2 + (i + 1) * (kDma - kDma / 2) / NT; ++d)
-                        dma(d, kt + 1, 1 - u);
+                        dma(d, kt - 1 + kRing, buf == 0 ? kRing - 1 : buf - 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
             f0 = sa[j & 1] * sb0;
@@ -259,25 +324,31 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
             if (j == MT - 1) read_sb(min(kt + 1, nkb - 1));
         }
     };
-    // stage 0 whole, and the part of stage 1 that the last row tile of a stage
-    // before it would have loaded
 #pragma unroll
     for (int d = 0; d < kDma; ++d) dma(d, 0, 0);
     // meanwhile the weight block scales of the tile's two 128-channel halves (gate
     // and up, or channels n0.. and n0 + 128..), with the codes' 1/448^2
     {
-        const int nnb = (a.N + kBlock - 1) / kBlock;
-        const float* sb_lo = a.SCB + ((size_t)e * (MODE == kGateUp ? 2 : 1) * nnb + n0 / kBlock) * nkb;
-        const float* sb_hi = MODE == kGateUp ? sb_lo + (size_t)nnb * nkb : n0 + kBlock < a.N ? sb_lo + nkb : sb_lo;
+        const int nnb = (a.N + kBlock - 1) / kBlock, all_kb = (K + kBlock - 1) / kBlock;
+        const float* sb_lo = a.SCB + ((size_t)e * (MODE == kGateUp ? 2 : 1) * nnb + n0 / kBlock) * all_kb + kb0;
+        const float* sb_hi =
+            MODE == kGateUp ? sb_lo + (size_t)nnb * all_kb : n0 + kBlock < a.N ? sb_lo + all_kb : sb_lo;
         for (int i = tid; i < nkb; i += 64 * S::NW) {
             s_sb[i] = sb_lo[i] * kCodeScale;
-            s_sb[kMaxKb + i] = sb_hi[i] * kCodeScale;
+            if (S::kHalves == 2) s_sb[kMaxKb + i] = sb_hi[i] * kCodeScale;
         }
     }
-    __builtin_amdgcn_s_waitcnt(0);
-    stage_barrier();
+    // then the ring's other stages but the last, and the part of that one that the
+    // last row tile of a stage before would have loaded
 #pragma unroll
-    for (int d = 0; d < kDma / 2; ++d) dma(d, 1, 1);
+    for (int t = 1; t < kRing - 1; ++t)
+#pragma unroll
+        for (int d = 0; d < kDma; ++d) dma(d, t, t);
+#pragma unroll
+    for (int d = 0; d < kDma / 2; ++d) dma(d, kRing - 1, kRing - 1);
+    wait_vmcnt<(kRing - 2) * kDma + kDma / 2>();  // stage 0
+    __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0)
+    stage_barrier();
 #pragma unroll
     for (int i = 0; i < NT; ++i) w[i] = frag(at_w, 16 * i);
     x[0] = frag(at_x, 0);
@@ -293,6 +364,13 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
     // ring, free now) as whole 16-byte pieces of rows.
     const int cq = (lane >> 4) * 4;
     __syncthreads();  // every wave's loads and reads of the ring are done
+    if constexpr (S::kSplit) {
+        if (a.split > 1) {
+            const bool last = split_sum<S::NW>(acc, tile, a.split, a.split_ws, a.split_tiles, wm * kWaveM < rows, wave,
+                                               lane, s_sa);
+            if (!last) return;
+        }
+    }
     if constexpr (MODE != kGateUp) {
         // 16-bit values of the wave's 64 channels, 128 bytes per row: piece c of row
         // r in slot c ^ ((r / 2) % 8)
@@ -322,7 +400,7 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
         } else {
             // a row's 128 channels (two waves) as 16-bit integers of their largest
             float* red = s_sb;  // [WN][BM], past its use
-            static_assert(S::WN * S::BM <= 2 * kMaxKb, "room for the maxima");
+            static_assert(MODE == kDense || S::WN * S::BM <= S::kHalves * kMaxKb, "room for the maxima");
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 float m = 0.0f;
@@ -415,18 +493,33 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
     }
 }
 
+__global__ __launch_bounds__(256) void clear_counters_kernel(uint32_t* counters, int n) {
+    for (int i = threadIdx.x; i < n; i += 256) counters[i] = 0;
+}
+
 template <typename S, int MODE, bool BF16>
 __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a) {
-    __shared__ __align__(1024) int8_t ring[2 * S::kStageBytes];
-    __shared__ float s_sa[2 * S::kSa];
-    __shared__ float s_sb[2 * kMaxKb];
+    __shared__ __align__(1024) int8_t ring[S::kStages * S::kStageBytes];
+    __shared__ float s_sa[S::kStages * S::kSa];
+    __shared__ float s_sb[S::kHalves * kMaxKb];
     constexpr int chans = MODE == kGateUp ? S::BN / 2 : S::BN;  // output channels of a tile
     const int tiles_n = (a.N + chans - 1) / chans;
     Tile t;
+    t.kb0 = 0;
+    t.nkb = (a.K + kBlock - 1) / kBlock;
     if constexpr (MODE == kDense) {
         constexpr int kGroupM = 4;  // tile rows that share a weight panel in L2
         const int tiles_m = (int)(((int64_t)a.M + a.tile_rows - 1) / a.tile_rows);
-        const int L = xcd_order(blockIdx.x, tiles_m * tiles_n);
+        const int split = S::kSplit ? a.split : 1;
+        int L = xcd_order(blockIdx.x, tiles_m * tiles_n * split);
+        if (S::kSplit) {
+            const int all = t.nkb;
+            t.part = L % split;
+            L /= split;
+            t.index = L;
+            t.kb0 = (int)((int64_t)t.part * all / split);
+            t.nkb = (int)((int64_t)(t.part + 1) * all / split) - t.kb0;
+        }
         const int first = L / (kGroupM * tiles_n) * kGroupM;
         const int gsz = min(tiles_m - first, kGroupM), in = L - first * tiles_n;
         t.row0 = (first + in % gsz) * a.tile_rows;
@@ -459,13 +552,15 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
     }
 }
 
-typedef Shape<2, 4, 8> TileBig;    // up to 256 rows, 8 waves
-typedef Shape<1, 4, 2> TileSmall;  // up to 32 rows, 4 waves
+typedef Shape<2, 4, 8, 2> TileBig;        // up to 256 rows x 256 channels, 8 waves
+typedef Shape<4, 2, 4, 3> TileTall;       // 256 x 128, 8 waves
+typedef Shape<4, 2, 2, 4, true> TileMid;  // 128 x 128, 8 waves; K may be split
+typedef Shape<1, 4, 2, 2> TileSmall;      // up to 32 rows x 256, 4 waves (experts)
 
 template <typename S, int MODE>
 hipError_t launch(const BlockGemmArgs& a, int64_t tiles_m, hipStream_t stream) {
     const int chans = MODE == kGateUp ? S::BN / 2 : S::BN;
-    const int64_t grid = tiles_m * ((a.N + chans - 1) / chans);
+    const int64_t grid = tiles_m * ((a.N + chans - 1) / chans) * (S::kSplit ? a.split : 1);
     if (grid > kMaxGrid) return hipErrorInvalidValue;
     if (a.bf16 && MODE == kDense)
         gemm_block_kernel<S, MODE, true><<<dim3((unsigned)grid), 64 * S::NW, 0, stream>>>(a);
@@ -474,46 +569,97 @@ hipError_t launch(const BlockGemmArgs& a, int64_t tiles_m, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Rows of a dense product's tiles: 64, 128, 192 or 256, whichever takes the least
-// time in rounds of the 256 CUs.  A tile's K stage is bound by LDS traffic: the
-// weights' 96 KiB (written once, read by both wave rows) and 40 KiB for each 64
-// rows.
-int dense_tile_rows(int64_t M, int64_t N) {
-    const int64_t tiles_n = (N + TileBig::BN - 1) / TileBig::BN;
-    int best = 256;
-    int64_t least = INT64_MAX;
-    for (int rows = 256; rows >= 64; rows -= 64) {
-        const int64_t rounds = ((M + rows - 1) / rows * tiles_n + 255) / 256;
-        const int64_t time = rounds * (96 + 40 * (rows / 64));
-        if (time < least) {
-            least = time;
-            best = rows;
-        }
-    }
+// How a dense product runs: the choice with the least estimated time in ns,
+// rounds of its workgroups over the CUs times (K stages + a fixed cost).  The
+// costs are fitted to measured products (a stage is bound by the bytes through
+// LDS and, in the wide tiles, by power): TileBig with 64, 128, 192 or 256 rows,
+// TileTall, TileMid, the streaming kernel.  TileMid may split K over workgroups
+// while tiles leave CUs idle; a split pays for its parts' way through memory.
+// Measured (us), the choice against the others: 64 x 28672 x 8192 TileMid 52,
+// streaming 83, TileBig 86; 1000 x 4096 x 4096 TileMid 22, TileTall 30, TileBig
+// 46; 2048 x 4096 x 4096 TileTall 39, TileMid 47, TileBig 49; 512 x 28672 x 8192
+// TileBig 117, TileTall 134; 64 x 4096 x 4096 TileMid in 4 parts 11, one 20,
+// streaming 16; 32 x 4096 x 4096 streaming 9, in 4 parts 11.
+enum Kind { kTileBig, kTileTall, kTileMid, kStream };
+struct DenseChoice {
+    Kind kind = kTileBig;
+    int rows = 256, split = 1;
+    int64_t time = INT64_MAX;
+};
+
+int64_t mid_tiles(int64_t M, int64_t N) {
+    return (M + TileMid::BM - 1) / TileMid::BM * ((N + TileMid::BN - 1) / TileMid::BN);
+}
+
+DenseChoice dense_choice(int64_t M, int64_t N, int64_t K) {
+    const int64_t stages = (K + kStageK - 1) / kStageK;
+    DenseChoice best;
+    auto consider = [&](Kind kind, int rows, int chans, int split, int64_t stage, int64_t fixed) {
+        const int64_t tiles = (M + rows - 1) / rows * ((N + chans - 1) / chans) * split;
+        const int64_t time = (tiles + 255) / 256 * ((stages + split - 1) / split * stage + fixed);
+        if (time < best.time) best = {kind, rows, split, time};
+    };
+    constexpr int64_t kBigStage[4] = {850, 1050, 1320, 1700};
+    for (int u = 4; u >= 1; --u) consider(kTileBig, 64 * u, TileBig::BN, 1, kBigStage[u - 1], 5000);
+    consider(kTileTall, TileTall::BM, TileTall::BN, 1, 1100, 4000);
+    consider(kTileMid, TileMid::BM, TileMid::BN, 1, 600, 3500);
+    for (int split = 2; split <= kBlockSplitMax && mid_tiles(M, N) * split <= 256 && 2 * split <= stages; ++split)
+        consider(kTileMid, TileMid::BM, TileMid::BN, split, 500, 8000 + 250 * split);
+    const int64_t stream = gemm_block_stream_time(M, N, K);
+    if (stream < best.time) best = {kStream, 0, 1, stream};
     return best;
 }
 
-}  // namespace
-
-size_t gemm_block_workspace(int64_t, int64_t, int64_t) { return 0; }
-
-hipError_t launch_gemm_block(const BlockGemmArgs& in, void* workspace, hipStream_t stream) {
-    (void)workspace;
-    if (gemm_block_streams(in.M, in.N, in.K)) return launch_gemm_block_stream(in, stream);
+template <typename S>
+hipError_t launch_dense(const BlockGemmArgs& in, int tile_rows, hipStream_t stream) {
     BlockGemmArgs a = in;
-    a.tile_rows = dense_tile_rows(in.M, in.N);
+    a.tile_rows = tile_rows;
     // row blocks of the activations small enough for one launch's grid
-    const int64_t tiles_n = ((int64_t)a.N + TileBig::BN - 1) / TileBig::BN;
-    const int64_t most = kMaxGrid / tiles_n * a.tile_rows;
+    const int64_t tiles_n = ((int64_t)a.N + S::BN - 1) / S::BN;
+    const int64_t most = kMaxGrid / tiles_n * tile_rows;
     for (int64_t m = 0; m < in.M; m += most) {
         a.M = (int)(in.M - m < most ? in.M - m : most);
         a.CA = in.CA + m * a.K;
         a.SCA = in.SCA + m;
         a.Y = in.Y + m * a.N;
-        const hipError_t e = launch<TileBig, kDense>(a, ((int64_t)a.M + a.tile_rows - 1) / a.tile_rows, stream);
+        const hipError_t e = launch<S, kDense>(a, ((int64_t)a.M + tile_rows - 1) / tile_rows, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+}  // namespace
+
+// A split product's arrival counters, then its parts.
+size_t gemm_block_workspace(int64_t M, int64_t N, int64_t K) {
+    if (M == 0 || N == 0) return 0;
+    const DenseChoice c = dense_choice(M, N, K);
+    if (c.split == 1) return 0;
+    const int64_t tiles = mid_tiles(M, N);
+    return split_counter_bytes((int)tiles) + (size_t)tiles * c.split * TileMid::BM * TileMid::BN * 4;
+}
+
+int gemm_block_counters(int64_t M, int64_t N, int64_t K) {
+    return dense_choice(M, N, K).split == 1 ? 0 : (int)mid_tiles(M, N);
+}
+
+hipError_t launch_gemm_block(const BlockGemmArgs& in, void* workspace, bool counters_cleared, hipStream_t stream) {
+    const DenseChoice c = dense_choice(in.M, in.N, in.K);
+    if (c.kind == kStream) return launch_gemm_block_stream(in, stream);
+    BlockGemmArgs a = in;
+    a.split = c.split;
+    if (c.split > 1) {
+        a.split_ws = workspace;
+        a.split_tiles = (int)mid_tiles(in.M, in.N);
+        if (!counters_cleared) {
+            clear_counters_kernel<<<1, 256, 0, stream>>>(static_cast<uint32_t*>(workspace), a.split_tiles);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    if (c.kind == kTileBig) return launch_dense<TileBig>(a, c.rows, stream);
+    if (c.kind == kTileTall) return launch_dense<TileTall>(a, c.rows, stream);
+    return launch_dense<TileMid>(a, c.rows, stream);
 }
 
 int grouped_tile_rows(int64_t pairs, int E) { return pairs / E > 48 ? TileBig::BM : TileSmall::BM; }

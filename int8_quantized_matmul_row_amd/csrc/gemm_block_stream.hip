@@ -328,7 +328,8 @@ __global__ __launch_bounds__(64 * kWaves8) void pair_down_kernel(const float* __
 template <int G, int C, int kDepth, bool BF16>
 __global__ __launch_bounds__(64 * kWaves8) void gemm_block_stream_kernel(BlockGemmArgs a) {
     constexpr int kN = 16 * C, kRedRow = kN + 4;
-    __shared__ __align__(16) float red[kWaves8 * 16 * kRedRow];
+    constexpr int kG = G * C <= 8 ? G : G / 2;  // row groups whose sums meet in LDS at once: up to 74 KiB
+    __shared__ __align__(16) float red[kWaves8 * kG * 16 * kRedRow];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int K = a.K, N = a.N, nkb = (K + kBlock - 1) / kBlock;
@@ -381,22 +382,25 @@ __global__ __launch_bounds__(64 * kWaves8) void gemm_block_stream_kernel(BlockGe
             fetch(d, i0 + d + kDepth);
         }
     }
-    // the waves' sums of 16 rows at a time, in wave order
+    // the waves' sums of kG row groups at a time, in wave order
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        if (g > 0) __syncthreads();
+    for (int g0 = 0; g0 < G; g0 += kG) {
+        if (g0 > 0) __syncthreads();
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            *reinterpret_cast<v4f*>(red + (wave * 16 + (lane & 15)) * kRedRow + 16 * c + 4 * (lane >> 4)) = acc[c][g];
+        for (int g = 0; g < kG; ++g)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                *reinterpret_cast<v4f*>(red + ((wave * kG + g) * 16 + (lane & 15)) * kRedRow + 16 * c +
+                                        4 * (lane >> 4)) = acc[c][g0 + g];
         __syncthreads();
-        for (int o = tid; o < 16 * kN; o += 64 * kWaves8) {
+        for (int o = tid; o < 16 * kG * kN; o += 64 * kWaves8) {
             const int r = o / kN, n = o % kN;
-            if (16 * g + r >= rows || n0 + n >= N) continue;
+            if (16 * g0 + r >= rows || n0 + n >= N) continue;
             float y = 0.0f;
 #pragma unroll
-            for (int v = 0; v < kWaves8; ++v) y += red[(v * 16 + r) * kRedRow + n];
+            for (int v = 0; v < kWaves8; ++v) y += red[(v * 16 * kG + r) * kRedRow + n];
             if (a.bias != nullptr) y += widen16<BF16>(a.bias[n0 + n]);
-            a.Y[(size_t)(m0 + 16 * g + r) * N + n0 + n] = narrow16<BF16>(y);
+            a.Y[(size_t)(m0 + 16 * g0 + r) * N + n0 + n] = narrow16<BF16>(y);
         }
     }
 }
@@ -479,23 +483,35 @@ hipError_t launch_experts_by_pair(const ExpertsArgs& a, float* H, hipStream_t st
     return hipGetLastError();
 }
 
-// Whether the product of M rows streams its weights, past the fused one's rows.
-bool gemm_block_streams(int64_t M, int64_t N, int64_t K) {
-    (void)K;
-    if (N > kMaxStreamN) return false;
-    if (M <= 64) return true;
-    const int64_t tiles = ((M + 127) / 128) * ((N + 255) / 256);
-    return tiles < 64;
+// Rows and channels of a workgroup of the streaming product, in units of 16.
+struct StreamShape {
+    int G, C;
+};
+static StreamShape stream_shape(int64_t M, int64_t N) {
+    if (M <= 16) return N >= 64 * 256 ? StreamShape{1, 4} : StreamShape{1, 1};
+    return M <= 32 ? StreamShape{2, 1} : StreamShape{4, 2};
+}
+
+// Its estimated time in ns: rounds of its workgroups times their latency, which
+// grows with the bytes a workgroup reads.
+int64_t gemm_block_stream_time(int64_t M, int64_t N, int64_t K) {
+    if (N > kMaxStreamN) return INT64_MAX;
+    const StreamShape s = stream_shape(M, N);
+    const int64_t groups = (M + 16 * s.G - 1) / (16 * s.G) * ((N + 16 * s.C - 1) / (16 * s.C));
+    if (groups > 1 << 20) return INT64_MAX;
+    const int64_t slots = s.G * s.C == 1 ? 512 : 256;  // workgroups that run at a time
+    const int64_t per_64 = s.G * s.C == 1 ? 90 : s.G == 1 ? 210 : s.G == 2 ? 102 : 166;  // ns per 64 of K
+    return (groups + slots - 1) / slots * (3000 + K / 64 * per_64);
 }
 
 hipError_t launch_gemm_block_stream(const BlockGemmArgs& a, hipStream_t stream) {
-    const bool wide = a.N >= 64 * 256;
-    if (a.M <= 16)
-        wide ? launch_codes<1, 4, 2>(a, stream) : launch_codes<1, 1, 4>(a, stream);
-    else if (a.M <= 32)
-        wide ? launch_codes<2, 4, 2>(a, stream) : launch_codes<2, 1, 4>(a, stream);
+    const StreamShape s = stream_shape(a.M, a.N);
+    if (s.G == 1)
+        s.C == 4 ? launch_codes<1, 4, 2>(a, stream) : launch_codes<1, 1, 4>(a, stream);
+    else if (s.G == 2)
+        launch_codes<2, 1, 4>(a, stream);
     else
-        wide ? launch_codes<4, 4, 1>(a, stream) : launch_codes<4, 2, 2>(a, stream);
+        launch_codes<4, 2, 2>(a, stream);
     return hipGetLastError();
 }
 

@@ -36,7 +36,10 @@ constexpr int kActBlocks = 4;
 
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_act_block_kernel(const uint16_t* __restrict__ X, int M, int K,
-                                                                 uint8_t* __restrict__ CA, float* __restrict__ SCA) {
+                                                                 uint8_t* __restrict__ CA, float* __restrict__ SCA,
+                                                                 uint32_t* __restrict__ clear, int n_clear) {
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < n_clear; i += 256) clear[i] = 0;
     const int grp = threadIdx.x >> 4, q = threadIdx.x & 15;
     const int nkb = (K + kBlock - 1) / kBlock;
     const int b0 = blockIdx.y * kActBlocks;
@@ -60,15 +63,15 @@ __global__ __launch_bounds__(256) void quantize_act_block_kernel(const uint16_t*
 }
 
 hipError_t launch_quantize_act_block(const void* X, bool bf16, int M, int K, uint8_t* CA, float* SCA,
-                                     hipStream_t stream) {
+                                     hipStream_t stream, uint32_t* clear, int n_clear) {
     const int nkb = (K + kBlock - 1) / kBlock;
     const int want = M / 16 + (M % 16 != 0);
     const dim3 grid((unsigned)(want < 65536 ? want : 65536), (unsigned)((nkb + kActBlocks - 1) / kActBlocks));
     const uint16_t* x = static_cast<const uint16_t*>(X);
     if (bf16)
-        quantize_act_block_kernel<true><<<grid, 256, 0, stream>>>(x, M, K, CA, SCA);
+        quantize_act_block_kernel<true><<<grid, 256, 0, stream>>>(x, M, K, CA, SCA, clear, n_clear);
     else
-        quantize_act_block_kernel<false><<<grid, 256, 0, stream>>>(x, M, K, CA, SCA);
+        quantize_act_block_kernel<false><<<grid, 256, 0, stream>>>(x, M, K, CA, SCA, clear, n_clear);
     return hipGetLastError();
 }
 

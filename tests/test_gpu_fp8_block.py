@@ -115,9 +115,43 @@ def test_product(M, N, K, dtype, bias):
     assert worst <= 1.0
 
 
+# (large tiles, tall tiles, K split over workgroups, a ragged edge of each)
+LARGE = [(2048, 4096, 320), (1000, 4096, 192), (512, 28672, 192), (257, 28700, 448), (64, 16384, 640),
+         (40, 600, 8192), (200, 300, 4160), (63, 4095, 4096), (4100, 1000, 192), (3000, 2050, 128), (129, 129, 2048),
+         (450, 8192, 576), (17, 100, 1344)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_product_at_sampled_outputs(M, N, K, dtype):
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    g = torch.Generator().manual_seed(M + N + K)
+    CA, CB = random_codes((M, K), M + 1).cuda(), random_codes((N, K), N + 2).cuda()
+    SCA = torch.exp2(4 * torch.rand(ref.blocks(K), M, generator=g) - 2)
+    SCB = 0.02 * torch.exp2(4 * torch.rand(ref.blocks(N), ref.blocks(K), generator=g) - 2)
+    b = torch.randn(N, generator=g).to(torch_dtype(dtype))
+    q = pkg.BlockAct(CA, SCA.cuda(), pkg.F16 if dtype == "f16" else pkg.BF16)
+    Y = pkg.matmul_fp8_block(q, CB, SCB.cuda(), bias=b.cuda())
+    rows = np.unique(np.r_[0, M - 1, np.random.default_rng(M).integers(0, M, 40)])
+    cols = np.unique(np.r_[0, N - 1, np.random.default_rng(N).integers(0, N, 60)])
+    A = values(CA[rows]) * ref.spread(SCA.numpy().T[rows], 1, len(rows), K)
+    W = values(CB[cols]) * ref.spread(SCB.numpy()[cols // 128], 1, len(cols), K)
+    want = A @ W.T + b.float().numpy().astype(np.float64)[cols]
+    bound = ref.product_bound(A, W, want)
+    err = np.abs(Y.float().cpu().numpy().astype(np.float64)[np.ix_(rows, cols)] - want)
+    worst = (err / (bound + 2 * ref.half_step16(np.abs(want) + bound, dtype == "bf16"))).max()
+    print(f"{M}x{N}x{K} {dtype}: worst error / bound {worst:.3f}", flush=True)
+    assert worst <= 1.0
+    # the same bits again (split K adds its parts in order)
+    again = pkg.matmul_fp8_block(q, CB, SCB.cuda(), bias=b.cuda())
+    assert torch.equal(Y, again)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 256, 512), (1, 200, 4160), (4, 128, 8192), (8, 96, 1024), (9, 300, 448), (16, 512, 192), (20, 130, 640),
-                                   (64, 200, 320), (70, 256, 1024), (300, 130, 192), (700, 300, 256)])
+                                   (64, 200, 320), (70, 256, 1024), (300, 130, 192), (700, 300, 256),
+                                   (40, 130, 4160)])
 def test_linear(M, N, K, dtype):
     """The one-call forward: codes as the quantizer gives them, then the product."""
     import int8_quantized_matmul_row_amd as pkg
