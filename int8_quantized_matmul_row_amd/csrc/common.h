@@ -607,7 +607,9 @@ struct RouteArgs {
     float scale;
     int32_t* ids;
     float* weights;
-    int group_lanes = 0;  // set by the launcher: lanes that share a group's ranking
+    // set by the launcher: lanes that hold a whole group (0: none do), and lanes that
+    // rank one together from LDS otherwise
+    int group_lanes = 0, rank_lanes = 0;
 };
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t stream);
 
@@ -653,7 +655,7 @@ int64_t gemm_block_stream_time(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_block_stream(const BlockGemmArgs& a, hipStream_t stream);
 bool linear_block_fused(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_block_fused(const BlockGemmArgs& a, const void* X, hipStream_t stream);
-int grouped_tile_rows(int64_t pairs, int E);
+int grouped_tile_rows(int64_t pairs, int E, int K, int I);
 hipError_t launch_experts_gate_up(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream);
 hipError_t launch_experts_down(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream);
 

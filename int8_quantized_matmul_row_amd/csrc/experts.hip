@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kMaxExperts = 1024;
+constexpr int kTileUnit = 64;  // rows: what a tile's time goes by, and the smallest tile
 
 // Exclusive prefix sum over kSortThreads values, one per thread; `waves` holds
 // the waves' sums.
@@ -50,11 +51,11 @@ __global__ __launch_bounds__(kSortThreads) void count_pairs_kernel(const int32_t
 // workgroup's part its row (in no particular order within an expert and part: a
 // row's results do not depend on its place); pairs whose id is outside [0, E)
 // get row -1.  The first workgroup lists the tiles: as few of at most
-// `tile_rows` rows as hold an expert's, of even size in units of `unit` rows.
+// `tile_rows` rows as hold an expert's, of even size in units of kTileUnit rows.
 // counts == nullptr: one part, counted here.
 __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
                                                                   int per_part, int top_k, int E, int tile_rows,
-                                                                  int unit, const int32_t* __restrict__ counts,
+                                                                  const int32_t* __restrict__ counts,
                                                                   int32_t* __restrict__ pair_row,
                                                                   int32_t* __restrict__ row_token,
                                                                   int32_t* __restrict__ tiles) {
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
         const int nt = (c + tile_rows - 1) / tile_rows;
         const int t0 = block_excl_scan(nt, waves, &total);
         if (tid == 0) tiles[0] = total;
-        const int step = nt > 0 ? ((c + unit - 1) / unit + nt - 1) / nt * unit : 0;
+        const int step = nt > 0 ? ((c + kTileUnit - 1) / kTileUnit + nt - 1) / nt * kTileUnit : 0;
         for (int t = 0; t < nt; ++t) {
             int32_t* out = tiles + 4 + 4 * (t0 + t);
             out[0] = tid;
@@ -184,7 +185,7 @@ ExpertsLayout layout(int64_t T, int E, int top_k, int K, int I) {
     L.counts = take((size_t)sort_parts(P) * E * 4);
     L.pair_row = take((size_t)P * 4);
     L.row_token = take((size_t)P * 4);
-    L.tiles = take(16 + 16 * (size_t)max_tiles(P, E, 32));
+    L.tiles = take(16 + 16 * (size_t)max_tiles(P, E, kTileUnit));
     L.h = take((size_t)P * I);
     L.sh = take((size_t)nib * P * 4);
     L.part = take((size_t)P * K * 2);
@@ -209,7 +210,7 @@ hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t str
     for (int64_t t0 = 0; t0 < a.T; t0 += L.tokens) {
         const int n = (int)(a.T - t0 < L.tokens ? a.T - t0 : L.tokens);
         const int P = n * a.top_k;
-        const int tile_rows = grouped_tile_rows(P, a.E);
+        const int tile_rows = grouped_tile_rows(P, a.E, a.K, a.I);
         uint8_t* ca = reinterpret_cast<uint8_t*>(ws + L.ca);
         float* sca = reinterpret_cast<float*>(ws + L.sca);
         int32_t* pair_row = reinterpret_cast<int32_t*>(ws + L.pair_row);
@@ -226,9 +227,8 @@ hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t str
         const int32_t* ids = a.ids + t0 * a.top_k;
         if (parts > 1)
             count_pairs_kernel<<<parts, kSortThreads, 0, stream>>>(ids, P, per_part, a.E, counts);
-        sort_pairs_kernel<<<parts, kSortThreads, 0, stream>>>(ids, P, per_part, a.top_k, a.E, tile_rows,
-                                                              tile_rows < 64 ? tile_rows : 64, counts, pair_row,
-                                                              row_token, tiles);
+        sort_pairs_kernel<<<parts, kSortThreads, 0, stream>>>(ids, P, per_part, a.top_k, a.E, tile_rows, counts,
+                                                              pair_row, row_token, tiles);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         BlockGemmArgs g;
         g.bf16 = a.bf16;

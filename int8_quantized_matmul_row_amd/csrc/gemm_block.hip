@@ -555,7 +555,7 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
 typedef Shape<2, 4, 8, 2> TileBig;        // up to 256 rows x 256 channels, 8 waves
 typedef Shape<4, 2, 4, 3> TileTall;       // 256 x 128, 8 waves
 typedef Shape<4, 2, 2, 4, true> TileMid;  // 128 x 128, 8 waves; K may be split
-typedef Shape<1, 4, 2, 2> TileSmall;      // up to 32 rows x 256, 4 waves (experts)
+typedef Shape<2, 4, 2, 3> TileLow;        // 64 x 256, 8 waves (experts of few rows)
 
 template <typename S, int MODE>
 hipError_t launch(const BlockGemmArgs& a, int64_t tiles_m, hipStream_t stream) {
@@ -578,8 +578,9 @@ hipError_t launch(const BlockGemmArgs& a, int64_t tiles_m, hipStream_t stream) {
 // Measured (us), the choice against the others: 64 x 28672 x 8192 TileMid 52,
 // streaming 83, TileBig 86; 1000 x 4096 x 4096 TileMid 22, TileTall 30, TileBig
 // 46; 2048 x 4096 x 4096 TileTall 39, TileMid 47, TileBig 49; 512 x 28672 x 8192
-// TileBig 117, TileTall 134; 64 x 4096 x 4096 TileMid in 4 parts 11, one 20,
-// streaming 16; 32 x 4096 x 4096 streaming 9, in 4 parts 11.
+// TileBig 117, TileTall 134; 64 x 4096 x 4096 TileMid in 8 parts 12, one 20,
+// streaming 15; 32 x 4096 x 4096 streaming 8, in 8 parts 11; 333 x 1001 x 4160
+// streaming 12, in 8 parts 15.
 enum Kind { kTileBig, kTileTall, kTileMid, kStream };
 struct DenseChoice {
     Kind kind = kTileBig;
@@ -604,7 +605,7 @@ DenseChoice dense_choice(int64_t M, int64_t N, int64_t K) {
     consider(kTileTall, TileTall::BM, TileTall::BN, 1, 1100, 4000);
     consider(kTileMid, TileMid::BM, TileMid::BN, 1, 600, 3500);
     for (int split = 2; split <= kBlockSplitMax && mid_tiles(M, N) * split <= 256 && 2 * split <= stages; ++split)
-        consider(kTileMid, TileMid::BM, TileMid::BN, split, 500, 8000 + 250 * split);
+        consider(kTileMid, TileMid::BM, TileMid::BN, split, 500, 8000 + 400 * split);
     const int64_t stream = gemm_block_stream_time(M, N, K);
     if (stream < best.time) best = {kStream, 0, 1, stream};
     return best;
@@ -662,16 +663,36 @@ hipError_t launch_gemm_block(const BlockGemmArgs& in, void* workspace, bool coun
     return launch_dense<TileMid>(a, c.rows, stream);
 }
 
-int grouped_tile_rows(int64_t pairs, int E) { return pairs / E > 48 ? TileBig::BM : TileSmall::BM; }
+// Rows of the grouped products' tiles: TileBig's or TileLow's, by the estimated
+// time of both products as in dense_choice, with every expert at the mean number
+// of rows and half a tile more for the uneven ends.  Few rows are bound by the
+// weights' way from memory, and there TileLow's deeper ring keeps more of them
+// under way.  Measured (us a call, K = 4096, I = 1024, TileLow against TileBig):
+// top 8 of 64 experts, 16 tokens 151 / 168, 128 tokens 197 / 206, 1024 tokens
+// 304 / 295, 2048 tokens 480 / 399; top 2 of 8, 512 tokens 54 / 78, 2048 tokens
+// 133 / 115.
+int grouped_tile_rows(int64_t pairs, int E, int K, int I) {
+    const int64_t used = pairs < E ? pairs : E, mean = (pairs + used - 1) / used;
+    auto time = [&](int rows, int64_t stage, int64_t fixed) {
+        const int64_t tiles = used * (2 * mean < rows ? 2 : 1 + 2 * mean / rows) / 2;
+        auto product = [&](int64_t n_tiles, int64_t depth) {
+            return (tiles * n_tiles + 255) / 256 * ((depth + kStageK - 1) / kStageK * stage + fixed);
+        };
+        return product((I + kBlock - 1) / kBlock, K) + product((K + TileBig::BN - 1) / TileBig::BN, I);
+    };
+    constexpr int64_t kBigStage[4] = {850, 1050, 1320, 1700};
+    const int u = (int)(mean >= 256 ? 4 : (mean + 63) / 64);
+    return time(TileLow::BM, 750, 4000) < time(TileBig::BM, kBigStage[u - 1], 5000) ? TileLow::BM : TileBig::BM;
+}
 
 hipError_t launch_experts_gate_up(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
     if (tile_rows == TileBig::BM) return launch<TileBig, kGateUp>(a, max_tiles, stream);
-    return launch<TileSmall, kGateUp>(a, max_tiles, stream);
+    return launch<TileLow, kGateUp>(a, max_tiles, stream);
 }
 
 hipError_t launch_experts_down(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
     if (tile_rows == TileBig::BM) return launch<TileBig, kDown>(a, max_tiles, stream);
-    return launch<TileSmall, kDown>(a, max_tiles, stream);
+    return launch<TileLow, kDown>(a, max_tiles, stream);
 }
 
 }  // namespace llmint8

@@ -493,14 +493,18 @@ static StreamShape stream_shape(int64_t M, int64_t N) {
 }
 
 // Its estimated time in ns: rounds of its workgroups times their latency, which
-// grows with the bytes a workgroup reads.
+// grows with the bytes a workgroup reads, faster where the rows of a fragment lie
+// a multiple of 2048 bytes apart and fall on the same memory channels (300 x 300
+// x 8192 27 us, x 8256 21).
 int64_t gemm_block_stream_time(int64_t M, int64_t N, int64_t K) {
     if (N > kMaxStreamN) return INT64_MAX;
     const StreamShape s = stream_shape(M, N);
     const int64_t groups = (M + 16 * s.G - 1) / (16 * s.G) * ((N + 16 * s.C - 1) / (16 * s.C));
     if (groups > 1 << 20) return INT64_MAX;
     const int64_t slots = s.G * s.C == 1 ? 512 : 256;  // workgroups that run at a time
-    const int64_t per_64 = s.G * s.C == 1 ? 90 : s.G == 1 ? 210 : s.G == 2 ? 102 : 166;  // ns per 64 of K
+    const bool same_channel = K % 2048 == 0;
+    const int64_t per_64 = s.G * s.C == 1 ? 90 : s.G == 1 ? 210  // ns per 64 of K
+                           : s.G == 2 ? (same_channel ? 85 : 60) : (same_channel ? 190 : 150);
     return (groups + slots - 1) / slots * (3000 + K / 64 * per_64);
 }
 

@@ -12,10 +12,15 @@
 // A logit of -inf or NaN takes the expert out for the token; a slot that no
 // expert is left for gets id -1 and weight 0.
 //
-// One wave per token: lane l holds experts l, l + 64, ...  A round of the
-// choice is a wave maximum of order-preserving integer keys; the lowest index
-// among equals falls out of the ballot of (key == maximum), expert row by
-// expert row.
+// One wave per token: lane l holds experts V l .. V l + V - 1, sorted by pick (order-
+// preserving integer keys) once.  A round of the choice is then a wave maximum of
+// the lanes' first keys; the lowest index among equals is the first lane of the
+// ballot of (key == maximum), which moves its next key up.  Bound by instruction
+// issue (16384 tokens of 256 experts in 8 groups, sigmoid and bias, top 8: about 490
+// vector instructions a token, 20 us; its bytes take 3.5): the scores (exp and an
+// exact division) are a fifth of it, the rounds a third.  They are computed for
+// every expert only where all are needed (a bias, or softmax weights that are not
+// renormalized); otherwise lane j recomputes slot j's from its logit.
 #include "common.h"
 
 namespace llmint8 {
@@ -33,10 +38,42 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __builtin_bit_cast(float, k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+// sum over lanes 0 .. 31
+__device__ __forceinline__ float half_wave_sum(float v) {
+    v += __builtin_bit_cast(float, dpp_i<0xB1>(0, __builtin_bit_cast(int, v)));   // xor 1
+    v += __builtin_bit_cast(float, dpp_i<0x4E>(0, __builtin_bit_cast(int, v)));   // xor 2
+    v += __builtin_bit_cast(float, dpp_i<0x141>(0, __builtin_bit_cast(int, v)));  // the other half of 8
+    v += __builtin_bit_cast(float, dpp_i<0x140>(0, __builtin_bit_cast(int, v)));  // the other half of 16
+    const int b = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0)) +
+           __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
+}
+
 __device__ __forceinline__ float wave_add(float v) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
     return v;
+}
+
+// maximum over the wave, as a scalar: prefix maxima in place (a lane without a
+// source keeps its own) to lane 63.  A register written by one instruction may be
+// read across lanes two wait states later.
+__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
+    asm("s_nop 1\n\t"
+        "v_max_u32_dpp %0, %0, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\t"
+        "v_max_u32_dpp %0, %0, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\t"
+        "v_max_u32_dpp %0, %0, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\t"
+        "v_max_u32_dpp %0, %0, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\t"
+        "v_max_u32_dpp %0, %0, %0 row_bcast:15 row_mask:0xa bank_mask:0xf\n\t"
+        "s_nop 1\n\t"
+        "v_max_u32_dpp %0, %0, %0 row_bcast:31 row_mask:0xc bank_mask:0xf\n\t"
+        "s_nop 1"
+        : "+v"(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 template <int DT>  // LLMINT8_F16, LLMINT8_BF16, LLMINT8_F32
@@ -47,54 +84,129 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
         return widen16<DT == LLMINT8_BF16>(static_cast<const uint16_t*>(p)[i]);
 }
 
+// V logits of one lane, adjacent and aligned to their size
+template <int DT, int V>
+__device__ __forceinline__ void load_logits(const void* p, int64_t i, float (&l)[V]) {
+    if constexpr (DT == LLMINT8_F32) {
+        __builtin_memcpy(l, __builtin_assume_aligned(static_cast<const float*>(p) + i, V * 4), V * 4);
+    } else {
+        uint16_t x[V];
+        __builtin_memcpy(x, __builtin_assume_aligned(static_cast<const uint16_t*>(p) + i, V * 2), V * 2);
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = widen16<DT == LLMINT8_BF16>(x[v]);
+    }
+}
+
 constexpr int kRouteWaves = 4;
 
-// One token; keys: this wave's E words of LDS (used with groups only).
-template <int DT, int V>  // V: experts per lane, E <= 64 V
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, uint32_t* keys) {
-    float l[V];
-    bool alive[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = 64 * v + lane;
-        l[v] = e < a.E ? load_logit<DT>(a.logits, t * a.E + e) : -__builtin_inff();
-        alive[v] = l[v] > -__builtin_inff();  // false for NaN
+// The groups to keep, as a mask of their first lanes: group g's best and next key
+// are the maxima over lanes g P .. g P + P - 1 (P a power of two).
+__device__ __forceinline__ uint64_t keep_groups(const RouteArgs& a, uint32_t best, uint32_t next, int P, int lane) {
+    auto merge = [&](uint32_t b, uint32_t n) {
+        next = max(max(next, n), min(best, b));
+        best = max(best, b);
+    };
+    // (the neighbours' halves mirrored: within a merged part all lanes agree)
+    if (P >= 2) merge((uint32_t)dpp_i<0xB1>(0, (int)best), (uint32_t)dpp_i<0xB1>(0, (int)next));
+    if (P >= 4) merge((uint32_t)dpp_i<0x4E>(0, (int)best), (uint32_t)dpp_i<0x4E>(0, (int)next));
+    if (P >= 8) merge((uint32_t)dpp_i<0x141>(0, (int)best), (uint32_t)dpp_i<0x141>(0, (int)next));
+    if (P >= 16) merge((uint32_t)dpp_i<0x140>(0, (int)best), (uint32_t)dpp_i<0x140>(0, (int)next));
+    if (P >= 32) merge(__shfl_xor(best, 16), __shfl_xor(next, 16));
+    if (P >= 64) merge(__shfl_xor(best, 32), __shfl_xor(next, 32));
+    uint32_t rank = best;
+    if (a.bias != nullptr) {
+        const float two = key_value(best) + key_value(next);
+        rank = next == 0 ? best : two == two ? order_key(two) : 0u;
     }
-    // scores; softmax's are left unnormalized (total holds their sum)
-    float s[V], total = 1.0f;
-    if (a.sigmoid) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-l[v]));
+    // a group stays if fewer than topk_group are ahead of it: ranked above, or
+    // equal with a lower index
+    const uint64_t first = __ballot((lane & (P - 1)) == 0 && lane < a.n_group * P);
+    uint64_t kept = 0;
+    for (int o = 0; o < a.n_group; ++o) {
+        const uint32_t r = (uint32_t)__builtin_amdgcn_readlane((int)rank, o * P);
+        const uint64_t before = ((uint64_t)1 << (o * P)) - 1;
+        const uint64_t ahead = first & (__ballot(rank > r) | (__ballot(rank == r) & before));
+        if (__builtin_popcountll(ahead) < a.topk_group) kept |= (uint64_t)1 << (o * P);
+    }
+    return kept;
+}
+
+// A lane's logits of token t (past E: some other expert's)
+template <int DT, int V, bool WHOLE>
+__device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int lane, float (&l)[V]) {
+    const int64_t row = t * a.E;
+    if constexpr (WHOLE) {
+        load_logits<DT, V>(a.logits, row + min(V * lane, a.E - V), l);
     } else {
-        float top = -__builtin_inff();
 #pragma unroll
-        for (int v = 0; v < V; ++v) top = alive[v] ? fmaxf(top, l[v]) : top;
+        for (int v = 0; v < V; ++v) l[v] = load_logit<DT>(a.logits, row + min(V * lane + v, a.E - 1));
+    }
+}
+
+// One token, its logits in l; keys: this wave's E words of LDS (used only for groups whose ranking
+// does not stay within whole lanes: group_lanes == 0).
+template <int DT, int V, bool WHOLE>  // V: experts per lane, E <= 64 V; WHOLE: E is a multiple of V
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, float (&l)[V], uint32_t* keys) {
+    const int64_t row = t * a.E;
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = l[v] == l[v] && V * lane + v < a.E ? l[v] : -__builtin_inff();
+    float top = 0.0f;
+    if (!a.sigmoid) {
+        top = l[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) top = fmaxf(top, l[v]);
         top = wave_max(top);
-        total = 0.0f;
+    }
+    // softmax's scores are left unnormalized (l == top: also for an infinite
+    // maximum; a row of -inf gives 1, and no expert is chosen)
+    auto score = [&](float x) {
+        return a.sigmoid ? 1.0f / (1.0f + expf(-x)) : x == top ? 1.0f : expf(x - top);
+    };
+    float total = 1.0f;
+    float pick[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {  // (l == top: also for an infinite maximum)
-            s[v] = alive[v] ? (l[v] == top ? 1.0f : expf(l[v] - top)) : 0.0f;
-            total += s[v];
+    for (int v = 0; v < V; ++v) pick[v] = l[v];
+    if (a.bias != nullptr || !(a.sigmoid || a.renormalize)) {
+        float s[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = score(l[v]);
+        if (!a.sigmoid) {
+            total = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) total += s[v];
+            total = wave_add(total);
         }
-        total = wave_add(total);
+        if (a.bias != nullptr) {
+            float b[V];
+            if constexpr (WHOLE) {
+                load_logits<LLMINT8_F32, V>(a.bias, min(V * lane, a.E - V), b);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) b[v] = a.bias[min(V * lane + v, a.E - 1)];
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float p = (a.sigmoid ? s[v] : s[v] / total) + b[v];
+                pick[v] = l[v] > -__builtin_inff() ? p : -__builtin_inff();
+            }
+        }
     }
     uint32_t key[V];
+    int sub[V];  // the key's expert within the lane
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = 64 * v + lane;
-        float p = l[v];
-        if (a.bias != nullptr && e < a.E) p = (a.sigmoid ? s[v] : s[v] / total) + a.bias[e];
-        key[v] = alive[v] && p > -__builtin_inff() ? order_key(p) : 0u;
+        key[v] = pick[v] > -__builtin_inff() ? order_key(pick[v]) : 0u;  // (0 for NaN too)
+        sub[v] = v;
     }
-    if (a.n_group > 1) {
+    const int size = a.E / a.n_group;
+    if (a.n_group > 1 && a.group_lanes == 0) {  // (uniform)
+        // rank the groups from LDS: group g's keys are read by the P lanes g P ..
         wave_fence();  // the last token's reads
-        // group g's keys are read by the P lanes g P .. g P + P - 1
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (64 * v + lane < a.E) keys[64 * v + lane] = key[v];
+            if (V * lane + v < a.E) keys[V * lane + v] = key[v];
         wave_fence();
-        const int size = a.E / a.n_group;
-        const int P = a.group_lanes, g = lane / P;
+        const int P = a.rank_lanes, g = lane / P;
         uint32_t best = 0, next = 0;
         if (g < a.n_group)
             for (int j = lane - g * P; j < size; j += P) {
@@ -102,62 +214,60 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
                 next = max(next, min(best, k));
                 best = max(best, k);
             }
-        for (int m = 1; m < P; m <<= 1) {
-            const uint32_t b = __shfl_xor(best, m), n = __shfl_xor(next, m);
-            next = max(max(next, n), min(best, b));
-            best = max(best, b);
-        }
-        uint32_t rank = best;
-        if (a.bias != nullptr && next != 0) {
-            const float two = key_value(best) + key_value(next);
-            rank = two == two ? order_key(two) : 0u;
-        }
-        // groups ranked above this lane's, the lower index first among equals
-        int above = 0;
-        for (int o = 0; o < a.n_group; ++o) {
-            const uint32_t r = (uint32_t)__builtin_amdgcn_readlane((int)rank, o * P);
-            above += r > rank || (r == rank && o < g);
-        }
-        const uint64_t kept = __ballot(g < a.n_group && above < a.topk_group);
+        const uint64_t kept = keep_groups(a, best, next, P, lane);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = 64 * v + lane;
-            const int eg = e < a.E ? e / size : 0;
-            if (!((kept >> (eg * P)) & 1)) key[v] = 0;
+            const int e = V * lane + v;
+            if (e < a.E && !((kept >> (e / size * P)) & 1)) key[v] = 0;
         }
     }
+    // each lane's keys in descending order, equal ones in order of index
+    // (neighbours change places only when out of order)
+#pragma unroll
+    for (int pass = 0; pass < V; ++pass)
+#pragma unroll
+        for (int v = pass & 1; v + 1 < V; v += 2) {
+            const bool swap = key[v] < key[v + 1];
+            const uint32_t hi = swap ? key[v + 1] : key[v], lo = swap ? key[v] : key[v + 1];
+            const int hs = swap ? sub[v + 1] : sub[v], ls = swap ? sub[v] : sub[v + 1];
+            key[v] = hi;
+            key[v + 1] = lo;
+            sub[v] = hs;
+            sub[v + 1] = ls;
+        }
+    if (a.n_group > 1 && a.group_lanes > 0) {  // a group is group_lanes whole lanes
+        const int P = a.group_lanes;
+        const uint64_t kept = keep_groups(a, key[0], V > 1 ? key[V > 1] : 0u, P, lane);
+        const bool mine = (kept >> (lane / P * P)) & 1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = mine ? key[v] : 0u;
+    }
+    // the experts within the lane in that order, 4 bits each (16 of them: two words)
+    uint32_t order = 0, order_hi = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) (v < 8 ? order : order_hi) |= (uint32_t)sub[v] << (4 * (v & 7));
     // top_k rounds; lane j keeps slot j
     int my_id = -1;
-    float my_s = 0.0f;
     for (int j = 0; j < a.top_k; ++j) {
-        uint32_t m = key[0];
-#pragma unroll
-        for (int v = 1; v < V; ++v) m = max(m, key[v]);
-        m = wave_max_u32(m);
+        const uint32_t m = wave_top(key[0]);
         if (m == 0) break;  // (uniform) no expert is left
-        int id = -1;
+        const int at = __builtin_ctzll(__ballot(key[0] == m));
+        const int id = V * at + (__builtin_amdgcn_readlane((int)order, at) & 15);
+        my_id = lane == j ? id : my_id;
+        const bool won = lane == at;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const uint64_t hit = __ballot(key[v] == m);
-            if (id < 0 && hit != 0) {
-                const int at = __builtin_ctzll(hit);
-                id = 64 * v + at;
-                const float sv = __builtin_bit_cast(
-                    float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s[v]), at));
-                if (lane == at) key[v] = 0;
-                if (lane == j) {
-                    my_id = id;
-                    my_s = sv;
-                }
-            }
-        }
+        for (int v = 0; v < V; ++v) key[v] = won ? (v + 1 < V ? key[v + 1 < V ? v + 1 : 0] : 0u) : key[v];
+        const uint32_t carry = V > 8 ? order_hi << 28 : 0u;
+        order = won ? order >> 4 | carry : order;
+        if (V > 8) order_hi = won ? order_hi >> 4 : order_hi;
     }
-    float w = my_s;
+    float w = score(load_logit<DT>(a.logits, row + max(my_id, 0)));
+    w = my_id >= 0 ? w : 0.0f;
     if (a.renormalize) {
-        const float sum = wave_add(lane < a.top_k ? my_s : 0.0f);
-        w = sum > 0.0f ? my_s / sum : 0.0f;
+        const float sum = half_wave_sum(w);  // (0 in the lanes past top_k)
+        w = sum > 0.0f ? w / sum : 0.0f;
     } else if (!a.sigmoid) {
-        w = my_id >= 0 ? my_s / total : 0.0f;
+        w = my_id >= 0 ? w / total : 0.0f;
     }
     if (lane < a.top_k) {
         a.ids[t * a.top_k + lane] = my_id;
@@ -165,30 +275,52 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
     }
 }
 
-template <int DT, int V>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
-    extern __shared__ uint32_t keys_all[];  // groups only: E keys per wave
+template <int DT, int V, bool WHOLE>
+__global__ __launch_bounds__(64 * kRouteWaves, V <= 4 ? 6 : 4) void route_kernel(RouteArgs a) {
+    extern __shared__ uint32_t keys_all[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     // (waves run on their own: no workgroup barrier below)
-    for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < a.T; t += (int64_t)gridDim.x * kRouteWaves)
-        route_token<DT, V>(a, t, lane, keys_all + wave * a.E);
+    int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
+    if (t >= a.T) return;
+    const int64_t step = (int64_t)gridDim.x * kRouteWaves;
+    float next[V];
+    load_row<DT, V, WHOLE>(a, t, lane, next);
+    for (; t < a.T; t += step) {
+        float l[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = next[v];
+        load_row<DT, V, WHOLE>(a, min(t + step, a.T - 1), lane, next);  // under way meanwhile
+        route_token<DT, V, WHOLE>(a, t, lane, l, keys_all + wave * a.E);
+    }
+}
+
+// A wave sets up once (what depends on the lane and E alone, a fifth of a token's
+// instructions) for all its tokens and loads the next token's logits meanwhile.
+constexpr int kRouteGrid = 1536;
+
+template <int DT, int V>
+void launch_route_v(const RouteArgs& a, hipStream_t stream) {
+    const int64_t want = (a.T + kRouteWaves - 1) / kRouteWaves;
+    const dim3 grid((unsigned)(want < kRouteGrid ? want : kRouteGrid)), block(64 * kRouteWaves);
+    const size_t lds = a.n_group > 1 && a.group_lanes == 0 ? (size_t)kRouteWaves * a.E * 4 : 0;
+    if (a.E % V == 0)
+        route_kernel<DT, V, true><<<grid, block, lds, stream>>>(a);
+    else
+        route_kernel<DT, V, false><<<grid, block, lds, stream>>>(a);
 }
 
 template <int DT>
 hipError_t launch_route_dt(const RouteArgs& a, hipStream_t stream) {
-    const int64_t want = (a.T + kRouteWaves - 1) / kRouteWaves;
-    const dim3 grid((unsigned)(want < 65536 ? want : 65536)), block(64 * kRouteWaves);
-    const size_t lds = a.n_group > 1 ? (size_t)kRouteWaves * a.E * 4 : 0;
     if (a.E <= 64)
-        route_kernel<DT, 1><<<grid, block, lds, stream>>>(a);
+        launch_route_v<DT, 1>(a, stream);
     else if (a.E <= 128)
-        route_kernel<DT, 2><<<grid, block, lds, stream>>>(a);
+        launch_route_v<DT, 2>(a, stream);
     else if (a.E <= 256)
-        route_kernel<DT, 4><<<grid, block, lds, stream>>>(a);
+        launch_route_v<DT, 4>(a, stream);
     else if (a.E <= 512)
-        route_kernel<DT, 8><<<grid, block, lds, stream>>>(a);
+        launch_route_v<DT, 8>(a, stream);
     else
-        route_kernel<DT, 16><<<grid, block, lds, stream>>>(a);
+        launch_route_v<DT, 16>(a, stream);
     return hipGetLastError();
 }
 
@@ -196,9 +328,13 @@ hipError_t launch_route_dt(const RouteArgs& a, hipStream_t stream) {
 
 hipError_t launch_route(const RouteArgs& in, int dtype, hipStream_t stream) {
     RouteArgs a = in;
+    int V = 1;  // experts per lane, as launch_route_dt chooses
+    while (64 * V < a.E) V <<= 1;
+    const int size = a.E / a.n_group, lanes = size / V;
+    if (size % V == 0 && (lanes & (lanes - 1)) == 0) a.group_lanes = lanes;
     int pow2 = 1;
     while (pow2 < a.n_group) pow2 <<= 1;
-    a.group_lanes = 64 / pow2;
+    a.rank_lanes = 64 / pow2;
     if (dtype == LLMINT8_F32) return launch_route_dt<LLMINT8_F32>(a, stream);
     if (dtype == LLMINT8_BF16) return launch_route_dt<LLMINT8_BF16>(a, stream);
     return launch_route_dt<LLMINT8_F16>(a, stream);
