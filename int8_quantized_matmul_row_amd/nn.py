@@ -1,5 +1,6 @@
 """torch modules over the C ABI: an LLM.int8() linear layer, model conversion,
-a chained FFN block, and quantized-weight checkpoints.
+a chained FFN block, quantized-weight checkpoints, and a linear layer and a
+mixture-of-experts feed-forward block on block-scaled E4M3 weights.
 
 "A Gentle Introduction to 8-bit Matrix Multiplication for transformers at
 scale", section "Usage": the layer is built from 16-bit weights, is quantized
@@ -22,10 +23,11 @@ from typing import Iterable, Optional
 
 import torch
 
-from . import QuantizedAct, alloc_act, linear, linear_workspace, quantize_weight
+from . import (QuantizedAct, alloc_act, experts_fp8_block, linear, linear_fp8_block,
+               linear_workspace, quantize_weight, quantize_weight_fp8_block, route_experts)
 
 __all__ = ["Linear8bitLt", "replace_linear_with_8bit", "FFN8bit", "save_quantized",
-           "load_quantized"]
+           "load_quantized", "LinearFP8Block", "MoEFFN8bit"]
 
 
 class Linear8bitLt(torch.nn.Module):
@@ -200,6 +202,150 @@ class FFN8bit(torch.nn.Module):
             n = layer.last_outlier_count
             out[name] = None if n is None else int(n.item()) / layer.in_features
         return out
+
+
+class _BlockCodes(torch.nn.Module):
+    """A module that holds 16-bit weights until it is moved to a GPU, where
+    `_quantize` turns them into E4M3 codes and block scales once.  The buffers
+    named in `_codes` keep their types under any cast and only change device."""
+
+    _codes: tuple = ()
+
+    def _quantize(self):
+        raise NotImplementedError
+
+    @property
+    def quantized(self) -> bool:
+        return getattr(self, self._codes[0]) is not None
+
+    def _apply(self, fn, *args, **kwargs):
+        held = {name: getattr(self, name) for name in self._codes}
+        for name in self._codes:
+            setattr(self, name, None)
+        try:
+            super()._apply(fn, *args, **kwargs)
+        finally:
+            for name, t in held.items():
+                if t is not None:
+                    setattr(self, name, t.to(fn(torch.zeros(1, device=t.device)).device))
+        if not self.quantized:
+            self._quantize()
+        return self
+
+
+def _check16(dtype):
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"dtype must be float16 or bfloat16, got {dtype}")
+
+
+class LinearFP8Block(_BlockCodes):
+    """y = x W^T + b on E4M3 codes with one scale per 128 x 128 block of W and per 128
+    features of x (`CB` uint8 [out, in], `SCB` fp32), quantized when the module is
+    moved to a GPU.  in_features must be a multiple of 64."""
+
+    _codes = ("CB", "SCB")
+
+    def __init__(self, weight: torch.Tensor, bias: Optional[torch.Tensor] = None):
+        super().__init__()
+        _check16(weight.dtype)
+        self.out_features, self.in_features = weight.shape
+        if self.in_features % 64 != 0:
+            raise ValueError(f"in_features must be a multiple of 64, got {self.in_features}")
+        self.weight = torch.nn.Parameter(weight.detach(), requires_grad=False)
+        self.bias = None if bias is None else torch.nn.Parameter(bias.detach().to(weight.dtype),
+                                                                 requires_grad=False)
+        self.register_buffer("CB", None)
+        self.register_buffer("SCB", None)
+        self._quantize()
+
+    @classmethod
+    def from_linear(cls, lin: torch.nn.Linear) -> "LinearFP8Block":
+        return cls(lin.weight, lin.bias)
+
+    def _quantize(self):
+        if self.weight is not None and self.weight.is_cuda:
+            self.CB, self.SCB = quantize_weight_fp8_block(self.weight.data.contiguous())
+            self.weight = None
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if not self.quantized:
+            raise RuntimeError("LinearFP8Block runs on the GPU only: move it with .cuda() first")
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"input has {x.shape[-1]} features, expected {self.in_features}")
+        X = x.reshape(-1, self.in_features).contiguous()
+        return linear_fp8_block(X, self.CB, self.SCB, bias=self.bias).reshape(
+            *x.shape[:-1], self.out_features)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}, quantized={self.quantized}")
+
+
+class MoEFFN8bit(_BlockCodes):
+    """A mixture-of-experts feed-forward block: a 16-bit router, then the chosen
+    experts' down(silu(gate(x)) * up(x)) on E4M3 codes with block scales.
+
+    router [E, d_model], W_gate and W_up [E, d_ff, d_model], W_down
+    [E, d_model, d_ff], all 16-bit; balance_bias fp32 [E] or None sees the choice of
+    experts only.  scoring, n_group, topk_group, renormalize, scale: as
+    route_experts.  `keep` (forward) marks the tokens to route, the others (padding)
+    get zeros.  `last_ids` holds the last forward's experts [tokens, top_k] on the
+    device (no sync)."""
+
+    _codes = ("CB13", "SCB13", "CB2", "SCB2", "balance_bias")
+
+    def __init__(self, router, W_gate, W_up, W_down, top_k: int, balance_bias=None,
+                 scoring: str = "softmax", n_group: int = 1, topk_group: int = 1,
+                 renormalize: bool = True, scale: float = 1.0):
+        super().__init__()
+        for t in (router, W_gate, W_up, W_down):
+            _check16(t.dtype)
+        E, I, K = W_gate.shape
+        if W_up.shape != W_gate.shape or W_down.shape != (E, K, I) or router.shape != (E, K):
+            raise ValueError(f"router {tuple(router.shape)}, W_gate {tuple(W_gate.shape)}, W_up "
+                             f"{tuple(W_up.shape)} and W_down {tuple(W_down.shape)} do not belong together")
+        if K % 64 != 0 or I % 64 != 0:
+            raise ValueError(f"d_model and d_ff must be multiples of 64, got {K} and {I}")
+        self.d_model, self.d_ff, self.n_experts, self.top_k = K, I, E, top_k
+        self.route = dict(scoring=scoring, n_group=n_group, topk_group=topk_group,
+                          renormalize=renormalize, scale=scale)
+
+        def held(t):
+            return torch.nn.Parameter(t.detach(), requires_grad=False)
+
+        self.router = held(router)
+        self.W13 = held(torch.stack((W_gate.detach(), W_up.detach()), dim=1))
+        self.W2 = held(W_down)
+        for name in self._codes:
+            self.register_buffer(name, None)
+        if balance_bias is not None:
+            self.balance_bias = balance_bias.detach().float()
+        self.last_ids: Optional[torch.Tensor] = None
+        self._quantize()
+
+    def _quantize(self):
+        if self.W13 is not None and self.W13.is_cuda:
+            self.CB13, self.SCB13 = quantize_weight_fp8_block(self.W13.data.contiguous())
+            self.CB2, self.SCB2 = quantize_weight_fp8_block(self.W2.data.contiguous())
+            self.W13 = self.W2 = None
+
+    def forward(self, x: torch.Tensor, keep: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if not self.quantized:
+            raise RuntimeError("MoEFFN8bit runs on the GPU only: move it with .cuda() first")
+        if x.shape[-1] != self.d_model:
+            raise ValueError(f"input has {x.shape[-1]} features, expected {self.d_model}")
+        X = x.reshape(-1, self.d_model).contiguous()
+        logits = torch.nn.functional.linear(X, self.router)
+        if keep is not None:
+            logits = logits.masked_fill(~keep.reshape(-1, 1), float("-inf"))
+        ids, weights = route_experts(logits, self.top_k, bias=self.balance_bias, **self.route)
+        self.last_ids = ids
+        y = experts_fp8_block(X, ids, weights, self.CB13, self.SCB13, self.CB2, self.SCB2)
+        return y.reshape(x.shape)
+
+    def extra_repr(self) -> str:
+        return (f"d_model={self.d_model}, d_ff={self.d_ff}, n_experts={self.n_experts}, "
+                f"top_k={self.top_k}, quantized={self.quantized}")
 
 
 def save_quantized(module: torch.nn.Module, path: str) -> None:
