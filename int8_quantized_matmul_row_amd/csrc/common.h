@@ -42,6 +42,19 @@ __device__ __forceinline__ uint16_t narrow16(float f) {
     }
 }
 
+// two of them in one conversion, a in the lower half (also infinities and NaN)
+template <bool BF16>
+__device__ __forceinline__ uint32_t narrow16x2(float a, float b) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    const v2f v = {a, b};
+    if constexpr (BF16)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2bf));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2h));
+}
+
 // ---- magnitudes as 16-bit patterns ----------------------------------------
 // For finite fp16/bf16 values, |x| (sign bit cleared) orders like the bit
 // pattern read as an unsigned integer, so maxima and threshold tests can run on
@@ -501,7 +514,8 @@ __device__ __forceinline__ float silu(float g) {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
-// the experts' down product leaves as integers of at most this magnitude
+// the experts' down product leaves as integers of at most this magnitude (what
+// v_cvt_pknorm_i16_f32 makes of 1.0)
 constexpr float kPartMax = 32767.0f;
 
 // ---- launchers (each returns hipGetLastError() after its launches) --------

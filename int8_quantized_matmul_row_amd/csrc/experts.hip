@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const int16_t* __restrict_
         uint32_t out[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            out[q] = narrow16<BF16>(y[2 * q]) | (uint32_t)narrow16<BF16>(y[2 * q + 1]) << 16;
+            out[q] = narrow16x2<BF16>(y[2 * q], y[2 * q + 1]);
         *reinterpret_cast<uint4*>(Y + t * K + c) = make_uint4(out[0], out[1], out[2], out[3]);
     }
 }

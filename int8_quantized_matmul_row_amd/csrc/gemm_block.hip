@@ -375,10 +375,10 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
         // 16-bit values of the wave's 64 channels, 128 bytes per row: piece c of row
         // r in slot c ^ ((r / 2) % 8)
         int8_t* stage = ring + wave * kWaveM * 128;
-        auto put = [&](int i, int j, const uint16_t (&y)[4]) {
+        auto put = [&](int i, int j, uint32_t y01, uint32_t y23) {
             const int piece = (2 * i + (lane >> 5)) ^ (fr >> 1);
             *reinterpret_cast<uint2*>(stage + (16 * j + fr) * 128 + piece * 16 + ((lane >> 4) & 1) * 8) =
-                make_uint2(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16);
+                make_uint2(y01, y23);
         };
         const int n_wave = n0 + wn * kWaveN;
         if constexpr (MODE == kDense) {
@@ -390,12 +390,9 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
                     for (int v = 0; v < 4; ++v)
                         if (n_wave + 16 * i + cq + v < a.N) b[v] = widen16<BF16>(a.bias[n_wave + 16 * i + cq + v]);
 #pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    uint16_t y[4];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) y[v] = narrow16<BF16>(acc[i][j][v] + b[v]);
-                    put(i, j, y);
-                }
+                for (int j = 0; j < MT; ++j)
+                    put(i, j, narrow16x2<BF16>(acc[i][j][0] + b[0], acc[i][j][1] + b[1]),
+                        narrow16x2<BF16>(acc[i][j][2] + b[2], acc[i][j][3] + b[3]));
             }
         } else {
             // a row's 128 channels (two waves) as 16-bit integers of their largest
@@ -417,16 +414,14 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
             for (int j = 0; j < MT; ++j) {
                 const int r = wm * kWaveM + 16 * j + fr;
                 const float m = fmaxf(red[(wn & 2) * BM + r], red[((wn & 2) + 1) * BM + r]);
-                const float f = m == 0.0f ? 0.0f : fminf(kPartMax / m, 3.402823466e38f);
+                const float f = m == 0.0f ? 0.0f : fminf(1.0f / m, 3.402823466e38f);
                 if ((wn & 1) == 0 && lane < 16 && r < rows && n_wave < a.N)
                     a.part_scale[(int64_t)(n_wave / kBlock) * a.ld_part + row0 + r] = m * (1.0f / kPartMax);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    uint16_t y[4];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) y[v] = (uint16_t)(int16_t)__builtin_rintf(acc[i][j][v] * f);
-                    put(i, j, y);
-                }
+                for (int i = 0; i < NT; ++i)
+                    put(i, j,
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_i16(acc[i][j][0] * f, acc[i][j][1] * f)),
+                        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_i16(acc[i][j][2] * f, acc[i][j][3] * f)));
             }
         }
         wave_fence();
