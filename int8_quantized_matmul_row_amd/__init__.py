@@ -674,8 +674,11 @@ def _blocks(n: int) -> int:
 
 
 def _want(t, name, dtype, shape, device):
-    """t is a contiguous tensor of this type and shape on `device`."""
-    if t.dtype != dtype or t.shape != shape:
+    """t is a contiguous tensor of this type and shape on `device` (a GPU)."""
+    if (t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda
+            and t.is_contiguous()):
+        return
+    if t.dtype != dtype or tuple(t.shape) != shape:
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
     _need(t, name, device)
 

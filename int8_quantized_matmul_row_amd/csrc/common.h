@@ -508,6 +508,50 @@ __device__ __forceinline__ float block_factor(float a) {
     return a == 0.0f ? 0.0f : fminf(448.0f / a, 3.402823466e38f);
 }
 
+template <bool BF16>
+__device__ __forceinline__ float absmax8(const v8u16& v) {
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(widen16<BF16>(v[e])));
+    return a;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint2 codes8(const v8u16& v, float f) {
+    return make_uint2(e4m3_pack4(widen16<BF16>(v[0]), widen16<BF16>(v[1]), widen16<BF16>(v[2]), widen16<BF16>(v[3]), f),
+                      e4m3_pack4(widen16<BF16>(v[4]), widen16<BF16>(v[5]), widen16<BF16>(v[6]), widen16<BF16>(v[7]), f));
+}
+
+// Activations: 16 lanes hold one block of a row (8 values, one 16-byte load each)
+// and reduce its maximum among themselves; 16 such groups (tid = 0 .. 255) take 16
+// rows, so the block's scales go out as 16 consecutive floats of the block-major
+// SCA [ceil(K/128), M], and kActBlocks blocks of each row, whose loads are all in
+// flight together.
+constexpr int kActBlocks = 4;
+template <bool BF16>
+__device__ __forceinline__ void quantize_act_part(const uint16_t* __restrict__ X, int64_t M, int K,
+                                                  uint8_t* __restrict__ CA, float* __restrict__ SCA,
+                                                  int64_t row_group, int block_group, int tid) {
+    const int q = tid & 15, nkb = (K + kBlock - 1) / kBlock, b0 = block_group * kActBlocks;
+    const int64_t m = row_group * 16 + (tid >> 4);
+    if (m >= M) return;
+    v8u16 v[kActBlocks];
+#pragma unroll
+    for (int i = 0; i < kActBlocks; ++i) {
+        const int c = (b0 + i) * kBlock + 8 * q;
+        v[i] = c < K ? *reinterpret_cast<const v8u16*>(X + m * K + c) : v8u16{0, 0, 0, 0, 0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < kActBlocks; ++i) {
+        const int b = b0 + i, c = b * kBlock + 8 * q;
+        if (b >= nkb) break;
+        const float a = row16_max(absmax8<BF16>(v[i]));
+        const float f = block_factor(a);
+        if (c < K) *reinterpret_cast<uint2*>(CA + m * K + c) = codes8<BF16>(v[i], f);
+        if (q == 0) SCA[b * M + m] = a;
+    }
+}
+
 // g / (1 + exp(-g)) to a few fp32 roundings: exp2 and reciprocal in one
 // instruction each (a tile of the gate/up product takes 32768 of them)
 __device__ __forceinline__ float silu(float g) {

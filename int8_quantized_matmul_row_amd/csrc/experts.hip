@@ -31,10 +31,8 @@ __device__ __forceinline__ int block_excl_scan(int v, int* waves, int* total) {
 
 // The pairs are sorted by expert in two passes over equal parts of the pairs, one
 // workgroup each: every part's counts, then its rows.
-__global__ __launch_bounds__(kSortThreads) void count_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
-                                                                   int per_part, int E,
-                                                                   int32_t* __restrict__ counts) {
-    __shared__ int count[kMaxExperts];
+__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ ids, int pairs, int per_part, int E,
+                                            int32_t* __restrict__ counts, int* count) {
     const int tid = threadIdx.x;
     count[tid] = 0;
     __syncthreads();
@@ -53,18 +51,15 @@ __global__ __launch_bounds__(kSortThreads) void count_pairs_kernel(const int32_t
 // get row -1.  The first workgroup lists the tiles: as few of at most
 // `tile_rows` rows as hold an expert's, of even size in units of kTileUnit rows.
 // counts == nullptr: one part, counted here.
-__global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t* __restrict__ ids, int pairs,
-                                                                  int per_part, int top_k, int E, int tile_rows,
-                                                                  const int32_t* __restrict__ counts,
-                                                                  int32_t* __restrict__ pair_row,
-                                                                  int32_t* __restrict__ row_token,
-                                                                  int32_t* __restrict__ tiles) {
-    __shared__ int next[kMaxExperts], waves[kSortThreads / 64];
+__device__ __forceinline__ void sort_pairs(const int32_t* __restrict__ ids, int pairs, int parts, int per_part,
+                                           int top_k, int E, int tile_rows, const int32_t* __restrict__ counts,
+                                           int32_t* __restrict__ pair_row, int32_t* __restrict__ row_token,
+                                           int32_t* __restrict__ tiles, int* next, int* waves) {
     const int tid = threadIdx.x, part = blockIdx.x;
     int c = 0, before = 0;  // the expert's rows, and those of earlier parts
     if (counts != nullptr) {
         if (tid < E)
-            for (int g = 0; g < (int)gridDim.x; ++g) {
+            for (int g = 0; g < parts; ++g) {
                 const int n = counts[g * E + tid];
                 before += g < part ? n : 0;
                 c += n;
@@ -105,6 +100,40 @@ __global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(const int32_t*
         }
         pair_row[p] = row;
     }
+}
+
+struct SortArgs {
+    const int32_t* ids;
+    int pairs, parts, per_part, top_k, E, tile_rows;
+    int32_t *counts, *pair_row, *row_token, *tiles;
+};
+
+// X's codes and, in the first workgroups beside them, the sort of the pairs (one
+// part) or its counts: neither needs the other, and a small call is bound by its
+// launches.
+template <bool BF16>
+__global__ __launch_bounds__(kSortThreads) void experts_prepare_kernel(const uint16_t* __restrict__ X, int M, int K,
+                                                                       uint8_t* __restrict__ CA,
+                                                                       float* __restrict__ SCA, SortArgs s) {
+    __shared__ int next[kMaxExperts], waves[kSortThreads / 64];
+    if ((int)blockIdx.x < s.parts) {
+        if (s.parts == 1)
+            sort_pairs(s.ids, s.pairs, 1, s.pairs, s.top_k, s.E, s.tile_rows, nullptr, s.pair_row, s.row_token,
+                       s.tiles, next, waves);
+        else
+            count_pairs(s.ids, s.pairs, s.per_part, s.E, s.counts, next);
+        return;
+    }
+    // four row groups of 256 threads, the row groups of a column before the next
+    const int64_t groups = ((int64_t)M + 15) / 16;
+    const int64_t g = (int64_t)(blockIdx.x - s.parts) * 4 + (threadIdx.x >> 8);
+    quantize_act_part<BF16>(X, M, K, CA, SCA, g % groups, (int)(g / groups), threadIdx.x & 255);
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_pairs_kernel(SortArgs s) {
+    __shared__ int next[kMaxExperts], waves[kSortThreads / 64];
+    sort_pairs(s.ids, s.pairs, s.parts, s.per_part, s.top_k, s.E, s.tile_rows, s.counts, s.pair_row, s.row_token,
+               s.tiles, next, waves);
 }
 
 // Parts of the two-pass sort.  Up to 2048 pairs one workgroup does it all in one
@@ -220,15 +249,29 @@ hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t str
         float* sh = reinterpret_cast<float*>(ws + L.sh);
         uint16_t* part = reinterpret_cast<uint16_t*>(ws + L.part);
         float* part_scale = reinterpret_cast<float*>(ws + L.part_scale);
-        hipError_t e = launch_quantize_act_block(a.X + (size_t)t0 * a.K, a.bf16, n, a.K, ca, sca, stream);
+        SortArgs sort;
+        sort.ids = a.ids + t0 * a.top_k;
+        sort.pairs = P;
+        sort.parts = sort_parts(P);
+        sort.per_part = (P + sort.parts - 1) / sort.parts;
+        sort.top_k = a.top_k;
+        sort.E = a.E;
+        sort.tile_rows = tile_rows;
+        sort.counts = reinterpret_cast<int32_t*>(ws + L.counts);
+        sort.pair_row = pair_row;
+        sort.row_token = row_token;
+        sort.tiles = tiles;
+        const int64_t nkb = (a.K + kBlock - 1) / kBlock;
+        const int64_t units = ((int64_t)n + 15) / 16 * ((nkb + kActBlocks - 1) / kActBlocks);
+        const dim3 prepare((unsigned)(sort.parts + (units + 3) / 4));
+        const uint16_t* x = a.X + (size_t)t0 * a.K;
+        if (a.bf16)
+            experts_prepare_kernel<true><<<prepare, kSortThreads, 0, stream>>>(x, n, a.K, ca, sca, sort);
+        else
+            experts_prepare_kernel<false><<<prepare, kSortThreads, 0, stream>>>(x, n, a.K, ca, sca, sort);
+        hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        const int parts = sort_parts(P), per_part = (P + parts - 1) / parts;
-        int32_t* counts = parts > 1 ? reinterpret_cast<int32_t*>(ws + L.counts) : nullptr;
-        const int32_t* ids = a.ids + t0 * a.top_k;
-        if (parts > 1)
-            count_pairs_kernel<<<parts, kSortThreads, 0, stream>>>(ids, P, per_part, a.E, counts);
-        sort_pairs_kernel<<<parts, kSortThreads, 0, stream>>>(ids, P, per_part, a.top_k, a.E, tile_rows, counts,
-                                                              pair_row, row_token, tiles);
+        if (sort.parts > 1) sort_pairs_kernel<<<sort.parts, kSortThreads, 0, stream>>>(sort);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         BlockGemmArgs g;
         g.bf16 = a.bf16;

@@ -406,7 +406,6 @@ __global__ __launch_bounds__(64 * kWaves8) void gemm_block_stream_kernel(BlockGe
 }
 
 constexpr int kPairLds = 36 * 1024;  // four workgroups per CU
-constexpr int kMaxPairs = 64;  // tokens x slots that run pair by pair, at most
 constexpr int64_t kMaxStreamN = (int64_t)1 << 27;  // the grid's threads stay below 2^32
 constexpr int kFusedLds = 66 * 1024;  // two workgroups per CU
 
@@ -454,13 +453,17 @@ hipError_t launch_linear_block_fused(const BlockGemmArgs& a, const void* X, hipS
     return hipGetLastError();
 }
 
-// Whether the experts run pair by pair: few enough pairs that not many share an
-// expert (a shared one's weights are read again, from L2 at best), and a pair's
-// codes of X and of h fit the workgroup's LDS.  Top 8 of 64 experts, K = 4096,
-// I = 1024, against the sorted tiles: 5 tokens 92 against 115 us, 8 tokens 140
-// against 157.
+// Whether the experts run pair by pair, in two launches: few pairs, of which not
+// many share an expert (a shared one's weights are read again, from L2 at best) or
+// whose weights are few anyway; a pair's codes of X and of h fit the workgroup's
+// LDS.  Measured against the sorted tiles (us): top 8 of 64 experts, K = 4096, I =
+// 1024: 5 tokens 92 / 115, 8 tokens 133 / 157; top 2 of 8, K = 1024, I = 512: 8
+// tokens 16 / 22, 16 tokens 21 / 22, 32 tokens 38 / 22; top 2 of 32, K = 1024, I =
+// 256: 30 tokens 25 / 22.
 bool experts_by_pair(int64_t pairs, int E, int K, int I) {
-    if (pairs > kMaxPairs || pairs > E) return false;
+    const int64_t pair_bytes = (int64_t)3 * I * K;
+    if (pairs > 64 || (pairs > 32 && (pairs > E || pair_bytes < 4 << 20))) return false;
+    if (pairs > E && pairs * pair_bytes > 48 << 20) return false;
     const int64_t x_blocks = (K + kBlock * kWaves8 - 1) / (kBlock * kWaves8) * kWaves8;
     const int64_t h_blocks = (int64_t)((I + kBlock - 1) / kBlock) * kWaves8;
     return x_blocks * (kBlock + 4) <= kPairLds && h_blocks * (kBlock + 4) <= kPairLds;

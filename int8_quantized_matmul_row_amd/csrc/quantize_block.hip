@@ -11,55 +11,17 @@
 
 namespace llmint8 {
 
-template <bool BF16>
-__device__ __forceinline__ float absmax8(const v8u16& v) {
-    float a = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(widen16<BF16>(v[e])));
-    return a;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint2 codes8(const v8u16& v, float f) {
-    return make_uint2(e4m3_pack4(widen16<BF16>(v[0]), widen16<BF16>(v[1]), widen16<BF16>(v[2]), widen16<BF16>(v[3]), f),
-                      e4m3_pack4(widen16<BF16>(v[4]), widen16<BF16>(v[5]), widen16<BF16>(v[6]), widen16<BF16>(v[7]), f));
-}
-
 // ---- activations -----------------------------------------------------------
-// 16 lanes hold one block of a row (8 values, one 16-byte load each) and
-// reduce its maximum among themselves; a workgroup of 16 such groups takes 16
-// rows, so the block's scales go out as 16 consecutive floats of the
-// block-major SCA [ceil(K/128), M], and kActBlocks blocks of each row, whose
-// loads are all in flight together.  HBM-bound: 2MK read, MK + 4M ceil(K/128)
-// written.
-constexpr int kActBlocks = 4;
-
+// HBM-bound: 2MK read, MK + 4M ceil(K/128) written (quantize_act_part).
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_act_block_kernel(const uint16_t* __restrict__ X, int M, int K,
                                                                  uint8_t* __restrict__ CA, float* __restrict__ SCA,
                                                                  uint32_t* __restrict__ clear, int n_clear) {
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < n_clear; i += 256) clear[i] = 0;
-    const int grp = threadIdx.x >> 4, q = threadIdx.x & 15;
-    const int nkb = (K + kBlock - 1) / kBlock;
-    const int b0 = blockIdx.y * kActBlocks;
-    for (int64_t m = (int64_t)blockIdx.x * 16 + grp; m < M; m += (int64_t)gridDim.x * 16) {
-        v8u16 v[kActBlocks];
-#pragma unroll
-        for (int i = 0; i < kActBlocks; ++i) {
-            const int c = (b0 + i) * kBlock + 8 * q;
-            v[i] = c < K ? *reinterpret_cast<const v8u16*>(X + m * K + c) : v8u16{0, 0, 0, 0, 0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int i = 0; i < kActBlocks; ++i) {
-            const int b = b0 + i, c = b * kBlock + 8 * q;
-            if (b >= nkb) break;
-            const float a = row16_max(absmax8<BF16>(v[i]));
-            const float f = block_factor(a);
-            if (c < K) *reinterpret_cast<uint2*>(CA + m * K + c) = codes8<BF16>(v[i], f);
-            if (q == 0) SCA[(int64_t)b * M + m] = a;
-        }
-    }
+    const int64_t groups = ((int64_t)M + 15) / 16;
+    for (int64_t g = blockIdx.x; g < groups; g += gridDim.x)
+        quantize_act_part<BF16>(X, M, K, CA, SCA, g, blockIdx.y, threadIdx.x);
 }
 
 hipError_t launch_quantize_act_block(const void* X, bool bf16, int M, int K, uint8_t* CA, float* SCA,
