@@ -432,15 +432,19 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
             const int r = 8 * it + (lane >> 3);
             if (wm * kWaveM + r >= rows) continue;
             const v4i y = *reinterpret_cast<const v4i*>(stage + r * 128 + (piece ^ ((r >> 1) & 7)) * 16);
+            // whole pieces in one store at any alignment of a row (rows of N values
+            // are 16-byte aligned only for N % 8 == 0; value by value such products
+            // took twice as long), non-temporal: written once, past the caches that
+            // hold the operands (4096 x 28672 x 8192 794 -> 788 us)
+            typedef int v4i_2 __attribute__((ext_vector_type(4), aligned(2)));
             uint16_t* out = Y + (size_t)r * a.N + 8 * piece;
-            if ((a.N & 7) == 0) {
-                // non-temporal: written once, past the caches that hold the operands
-                // (4096 x 28672 x 8192 794 -> 788 us)
-                if (n_wave + 8 * piece < a.N) __builtin_nontemporal_store(y, reinterpret_cast<v4i*>(out));
+            const int left = a.N - n_wave - 8 * piece;
+            if (left >= 8) {
+                __builtin_nontemporal_store(y, reinterpret_cast<v4i_2*>(out));
             } else {
 #pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    if (n_wave + 8 * piece + v < a.N) out[v] = (uint16_t)((uint32_t)y[v >> 1] >> (16 * (v & 1)));
+                for (int v = 0; v < 7; ++v)
+                    if (v < left) out[v] = (uint16_t)((uint32_t)y[v >> 1] >> (16 * (v & 1)));
             }
         }
     } else {
