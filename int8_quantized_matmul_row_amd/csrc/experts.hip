@@ -59,6 +59,7 @@ __device__ __forceinline__ void sort_pairs(const int32_t* __restrict__ ids, int 
     int c = 0, before = 0;  // the expert's rows, and those of earlier parts
     if (counts != nullptr) {
         if (tid < E)
+#pragma unroll 8
             for (int g = 0; g < parts; ++g) {
                 const int n = counts[g * E + tid];
                 before += g < part ? n : 0;
@@ -161,15 +162,30 @@ __global__ __launch_bounds__(256) void combine_kernel(const int16_t* __restrict_
         float y[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) y[q] = 0.0f;
-#pragma unroll 4
-        for (int j = 0; j < top_k; ++j) {
-            const int row = pair_row[t * top_k + j];
-            if (row < 0) continue;
-            const float w = weights[t * top_k + j] * scale[row];
-            const v4i v = *reinterpret_cast<const v4i*>(part + (size_t)row * K + c);
+        // Four slots' loads under way at a time; an empty slot (or one past top_k)
+        // reads row 0, whose integers are finite whatever they are, with weight 0.
+        for (int j0 = 0; j0 < top_k; j0 += 4) {
+            int row[4];
+            float w[4];
+            v4i v[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                y[q] = __builtin_fmaf(w, (float)(int16_t)((uint32_t)v[q >> 1] >> (16 * (q & 1))), y[q]);
+            for (int u = 0; u < 4; ++u) {
+                const int64_t p = t * top_k + min(j0 + u, top_k - 1);
+                row[u] = j0 + u < top_k ? pair_row[p] : -1;
+                w[u] = weights[p];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int r = max(row[u], 0);
+                const float s = scale[r];
+                w[u] = row[u] >= 0 ? w[u] * s : 0.0f;
+                v[u] = *reinterpret_cast<const v4i*>(part + (size_t)r * K + c);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    y[q] = __builtin_fmaf(w[u], (float)(int16_t)((uint32_t)v[u][q >> 1] >> (16 * (q & 1))), y[q]);
         }
         uint32_t out[4];
 #pragma unroll

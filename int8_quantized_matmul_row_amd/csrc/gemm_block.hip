@@ -554,6 +554,7 @@ __global__ __launch_bounds__(64 * S::NW) void gemm_block_kernel(BlockGemmArgs a)
 typedef Shape<2, 4, 8, 2> TileBig;        // up to 256 rows x 256 channels, 8 waves
 typedef Shape<4, 2, 4, 3> TileTall;       // 256 x 128, 8 waves
 typedef Shape<4, 2, 2, 4, true> TileMid;  // 128 x 128, 8 waves; K may be split
+typedef Shape<2, 4, 4, 3> TileHalf;       // 128 x 256, 8 waves (experts)
 typedef Shape<2, 4, 2, 3> TileLow;        // 64 x 256, 8 waves (experts of few rows)
 
 template <typename S, int MODE>
@@ -662,14 +663,17 @@ hipError_t launch_gemm_block(const BlockGemmArgs& in, void* workspace, bool coun
     return launch_dense<TileMid>(a, c.rows, stream);
 }
 
-// Rows of the grouped products' tiles: TileBig's or TileLow's, by the estimated
-// time of both products as in dense_choice, with every expert at the mean number
-// of rows and half a tile more for the uneven ends.  Few rows are bound by the
-// weights' way from memory, and there TileLow's deeper ring keeps more of them
-// under way.  Measured (us a call, K = 4096, I = 1024, TileLow against TileBig):
-// top 8 of 64 experts, 16 tokens 151 / 168, 128 tokens 197 / 206, 1024 tokens
-// 304 / 295, 2048 tokens 480 / 399; top 2 of 8, 512 tokens 54 / 78, 2048 tokens
-// 133 / 115.
+// Rows of the grouped products' tiles, 64, 128 or 256, by the estimated time of
+// both products as in dense_choice, with every expert at the mean number of rows
+// and half a tile more for the uneven ends.  Few rows are bound by the weights'
+// way from memory, and there a deeper ring keeps more of them under way; where
+// the tiles do not fill the chip, smaller ones spread over more of it.
+// Measured (us a call, TileLow / TileHalf / TileBig):
+//   top 8 of 64 experts, K = 4096, I = 1024   128 tokens 189 / 199 / 200,
+//                        1024 tokens 305 / 276 / 292, 4096 tokens 842 / 680 / 599
+//   top 2 of 8 experts, K = 4096, I = 1024    512 tokens 49 / 52 / 68,
+//                        1024 tokens 81 / 72 / 82, 2048 tokens 135 / 126 / 118
+//   top 8 of 12 experts, K = 1280, I = 704    452 tokens 50 / 42 / 53
 int grouped_tile_rows(int64_t pairs, int E, int K, int I) {
     const int64_t used = pairs < E ? pairs : E, mean = (pairs + used - 1) / used;
     auto time = [&](int rows, int64_t stage, int64_t fixed) {
@@ -681,16 +685,20 @@ int grouped_tile_rows(int64_t pairs, int E, int K, int I) {
     };
     constexpr int64_t kBigStage[4] = {850, 1050, 1320, 1700};
     const int u = (int)(mean >= 256 ? 4 : (mean + 63) / 64);
-    return time(TileLow::BM, 750, 4000) < time(TileBig::BM, kBigStage[u - 1], 5000) ? TileLow::BM : TileBig::BM;
+    const int64_t big = time(TileBig::BM, kBigStage[u - 1], 5000), half = time(TileHalf::BM, 1100, 4500),
+                  low = time(TileLow::BM, 750, 4000);
+    return low <= half && low <= big ? TileLow::BM : half < big ? TileHalf::BM : TileBig::BM;
 }
 
 hipError_t launch_experts_gate_up(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
     if (tile_rows == TileBig::BM) return launch<TileBig, kGateUp>(a, max_tiles, stream);
+    if (tile_rows == TileHalf::BM) return launch<TileHalf, kGateUp>(a, max_tiles, stream);
     return launch<TileLow, kGateUp>(a, max_tiles, stream);
 }
 
 hipError_t launch_experts_down(const BlockGemmArgs& a, int tile_rows, int64_t max_tiles, hipStream_t stream) {
     if (tile_rows == TileBig::BM) return launch<TileBig, kDown>(a, max_tiles, stream);
+    if (tile_rows == TileHalf::BM) return launch<TileHalf, kDown>(a, max_tiles, stream);
     return launch<TileLow, kDown>(a, max_tiles, stream);
 }
 
