@@ -13,6 +13,8 @@ namespace llmint8 {
 
 // ---- activations -----------------------------------------------------------
 // HBM-bound: 2MK read, MK + 4M ceil(K/128) written (quantize_act_part).
+// 4096 x 8192 23.7 us (4.3 TB/s); 1000 x 4096 4.6 us and 32 x 8192 4.1, which are
+// the launch and one round trip through memory.
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_act_block_kernel(const uint16_t* __restrict__ X, int M, int K,
                                                                  uint8_t* __restrict__ CA, float* __restrict__ SCA,
@@ -40,7 +42,8 @@ hipError_t launch_quantize_act_block(const void* X, bool bf16, int M, int K, uin
 // ---- weights ---------------------------------------------------------------
 // One workgroup per 128 x 128 block (two rows of lanes per 256 bytes of a
 // weight row, 16 rows at a time): the block stays in registers between the
-// maximum and the codes, so W is read once.  HBM-bound: 2NK read, NK written.
+// maximum and the codes, so W is read once.  HBM-bound: 2NK read, NK written;
+// 28672 x 8192 124 us, 5.7 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(256) void quantize_weight_block_kernel(const uint16_t* __restrict__ W, int N, int K,
                                                                     uint8_t* __restrict__ CB,

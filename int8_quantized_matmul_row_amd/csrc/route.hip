@@ -17,7 +17,7 @@
 // the lanes' first keys; the lowest index among equals is the first lane of the
 // ballot of (key == maximum), which moves its next key up.  Bound by instruction
 // issue (16384 tokens of 256 experts in 8 groups, sigmoid and bias, top 8: about 490
-// vector instructions a token, 20 us; its bytes take 3.5): the scores (exp and an
+// vector instructions a token, 19.5 us; its bytes take 3.5; one token 2.7 us): the scores (exp and an
 // exact division) are a fifth of it, the rounds a third.  They are computed for
 // every expert only where all are needed (a bias, or softmax weights that are not
 // renormalized); otherwise lane j recomputes slot j's from its logit.
