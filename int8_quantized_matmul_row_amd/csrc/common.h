@@ -355,6 +355,9 @@ __device__ __forceinline__ uint32_t row16_max_u16x2(uint32_t v) {
     return v;
 }
 
+// maximum; NaN where either is (fmaxf drops it)
+__device__ __forceinline__ float nan_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 __device__ __forceinline__ float wave_max(float v) {
     v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0xB1>(0, __builtin_bit_cast(int, v))));   // xor 1
     v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x4E>(0, __builtin_bit_cast(int, v))));   // xor 2

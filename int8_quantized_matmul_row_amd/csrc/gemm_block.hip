@@ -403,7 +403,8 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
                         narrow16x2<BF16>(acc[i][j][2] + b[2], acc[i][j][3] + b[3]));
             }
         } else {
-            // a row's 128 channels (two waves) as 16-bit integers of their largest
+            // a row's 128 channels (two waves) as 16-bit integers of their largest.
+            // An integer cannot say NaN: the scale is NaN where one of them is.
             float* red = s_sb;  // [WN][BM], past its use
             static_assert(MODE == kDense || S::WN * S::BM <= S::kHalves * kMaxKb, "room for the maxima");
 #pragma unroll
@@ -412,16 +413,16 @@ __device__ __forceinline__ void tile_body(const BlockGemmArgs& a, const Tile& ti
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) m = fmaxf(m, fabsf(acc[i][j][v]));
-                m = fmaxf(m, __shfl_xor(m, 16));
-                m = fmaxf(m, __shfl_xor(m, 32));
+                    for (int v = 0; v < 4; ++v) m = nan_max(m, fabsf(acc[i][j][v]));
+                m = nan_max(m, __shfl_xor(m, 16));
+                m = nan_max(m, __shfl_xor(m, 32));
                 if (lane < 16) red[wn * BM + wm * kWaveM + 16 * j + lane] = m;
             }
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 const int r = wm * kWaveM + 16 * j + fr;
-                const float m = fmaxf(red[(wn & 2) * BM + r], red[((wn & 2) + 1) * BM + r]);
+                const float m = nan_max(red[(wn & 2) * BM + r], red[((wn & 2) + 1) * BM + r]);
                 const float f = m == 0.0f ? 0.0f : fminf(1.0f / m, 3.402823466e38f);
                 if ((wn & 1) == 0 && lane < 16 && r < rows && n_wave < a.N)
                     a.part_scale[(int64_t)(n_wave / kBlock) * a.ld_part + row0 + r] = m * (1.0f / kPartMax);

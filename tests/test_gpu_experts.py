@@ -173,3 +173,24 @@ def test_another_stream(T):
     got = [pkg.experts_fp8_block(x, ids, w, *q13, *q2, stream=s) for _ in range(4)]
     s.synchronize()
     assert all(torch.equal(y, want) for y in got)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("T,E,k,K,I", [(2, 64, 4, 256, 128), (40, 6, 2, 320, 192), (700, 3, 2, 256, 320)])
+def test_a_value_that_is_not_finite_shows_in_its_token_alone(T, E, k, K, I, value, dtype):
+    """One NaN or infinity in a token's X: a code that is NaN, hence NaN in all of
+    its g, u, h and outputs, whichever path runs; the other tokens' are untouched."""
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    x, q13, q2, *_ = make(T, E, K, I, dtype, 11)
+    ids = torch.arange(T * k, dtype=torch.int32).reshape(T, k) % E
+    weights = torch.full((T, k), 0.25)
+    was = pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2)
+    t = T // 2
+    x[t, K - 3] = float(value)
+    Y = pkg.experts_fp8_block(x, ids.cuda(), weights.cuda(), *q13, *q2)
+    print(f"finite outputs of the token: {int(torch.isfinite(Y[t]).sum())}", flush=True)
+    assert Y[t].isnan().all()
+    others = torch.arange(T, device="cuda") != t
+    assert torch.equal(Y[others], was[others]) and torch.isfinite(was).all()

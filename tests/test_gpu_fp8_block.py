@@ -222,3 +222,21 @@ def test_weight_past_two_gib(M):
     # every repetition of the 1000 rows gives the same outputs, up to the last block
     same = Y[:, : 269 * 1000].view(M, 269, 1000)
     assert torch.equal(same, same[:, :1].expand_as(same))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 192), (3, 300, 576), (33, 130, 4160), (300, 300, 320), (1200, 1000, 192)])
+def test_a_value_that_is_not_finite_shows_in_its_row_alone(M, N, K, value, dtype):
+    """One NaN or infinity in a row of X: a code that is NaN, hence NaN in all of the
+    row's outputs, whichever kernel runs; the other rows' are untouched."""
+    import torch
+    import int8_quantized_matmul_row_amd as pkg
+    x = rand((M, K), 1, dtype).cuda()
+    q = pkg.quantize_weight_fp8_block(rand((N, K), 2, dtype).cuda())
+    was = pkg.linear_fp8_block(x, *q)
+    x[M // 2, K - 3] = float(value)
+    Y = pkg.linear_fp8_block(x, *q)
+    assert Y[M // 2].isnan().all()
+    others = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(Y[others], was[others]) and torch.isfinite(was).all()
