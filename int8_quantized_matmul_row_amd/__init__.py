@@ -693,6 +693,8 @@ def _rows(t, name):
 def _out(out, shape, dtype, device, stream):
     """The caller's output tensor, checked, or a new one."""
     if out is None:
+        if stream is None:  # a shape in one argument takes 0.4 us longer to read
+            return _torch().empty(*shape, dtype=dtype, device=device)
         return _empty(shape, dtype, device, stream)
     _want(out, "out", dtype, shape, device)
     return out
