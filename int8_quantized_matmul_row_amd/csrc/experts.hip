@@ -149,43 +149,47 @@ int sort_parts(int64_t pairs) {
 
 // Y[t, :] = sum_j w[t, j] * part[row(t, j), :] * part_scale, in fp32 and in the
 // order of j, rounded once.  A thread holds 8 columns of one token.  Bound by the
-// bytes: 4096 tokens of 8 slots and 4096 columns 57-60 us, 5.1 TB/s.
-template <bool BF16>
+// bytes: 4096 tokens of 8 slots and 4096 columns 58-60 us, 5.1 TB/s; few tokens by
+// its two trips through memory (row numbers, then rows), which kSlots = 8 takes
+// once for up to 8 slots: 45 tokens of 6 slots and 2048 columns 6.1 us, 4 at a
+// time 6.5; up to 4 slots need no more.
+template <bool BF16, int kSlots>
 __global__ __launch_bounds__(256) void combine_kernel(const int16_t* __restrict__ part,
                                                       const float* __restrict__ part_scale, int64_t ld_part,
                                                       const int32_t* __restrict__ pair_row,
                                                       const float* __restrict__ weights, int T, int K, int top_k,
                                                       uint16_t* __restrict__ Y) {
-    const int per_row = K >> 3;
-    const int64_t items = (int64_t)T * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / per_row;
-        const int c = (int)(i - t * per_row) * 8;
+    const uint32_t per_row = (uint32_t)K >> 3;
+    const uint32_t items = (uint32_t)T * per_row;  // (a chunk's: below 2^27)
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < items; i += gridDim.x * 256) {
+        const uint32_t row_of = i / per_row;
+        const int64_t t = row_of;
+        const int c = (int)(i - row_of * per_row) * 8;
         const float* scale = part_scale + (c / kBlock) * ld_part;
         float y[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) y[q] = 0.0f;
-        // Four slots' loads under way at a time; an empty slot (or one past top_k)
+        // kSlots slots' loads under way at a time; an empty slot (or one past top_k)
         // reads row 0, whose integers are finite whatever they are, with weight 0.
-        for (int j0 = 0; j0 < top_k; j0 += 4) {
-            int row[4];
-            float w[4];
-            v4i v[4];
+        for (int j0 = 0; j0 < top_k; j0 += kSlots) {
+            int row[kSlots];
+            float w[kSlots];
+            v4i v[kSlots];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kSlots; ++u) {
                 const int64_t p = t * top_k + min(j0 + u, top_k - 1);
                 row[u] = j0 + u < top_k ? pair_row[p] : -1;
                 w[u] = weights[p];
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kSlots; ++u) {
                 const int r = max(row[u], 0);
                 const float s = scale[r];
                 w[u] = row[u] >= 0 ? w[u] * s : 0.0f;
                 v[u] = *reinterpret_cast<const v4i*>(part + (size_t)r * K + c);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < kSlots; ++u)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     y[q] = __builtin_fmaf(w[u], (float)(int16_t)((uint32_t)v[u][q >> 1] >> (16 * (q & 1))), y[q]);
@@ -325,12 +329,10 @@ hipError_t launch_experts(const ExpertsArgs& a, void* workspace, hipStream_t str
         const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
         uint16_t* y = a.Y + (size_t)t0 * a.K;
         const float* w = a.weights + t0 * a.top_k;
-        if (a.bf16)
-            combine_kernel<true><<<grid, 256, 0, stream>>>(reinterpret_cast<const int16_t*>(part), part_scale, P, pair_row,
-                                                           w, n, a.K, a.top_k, y);
-        else
-            combine_kernel<false><<<grid, 256, 0, stream>>>(reinterpret_cast<const int16_t*>(part), part_scale, P, pair_row,
-                                                           w, n, a.K, a.top_k, y);
+        const auto combine = a.bf16 ? (a.top_k <= 4 ? combine_kernel<true, 4> : combine_kernel<true, 8>)
+                                    : (a.top_k <= 4 ? combine_kernel<false, 4> : combine_kernel<false, 8>);
+        combine<<<grid, 256, 0, stream>>>(reinterpret_cast<const int16_t*>(part), part_scale, P, pair_row, w, n, a.K,
+                                          a.top_k, y);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;
